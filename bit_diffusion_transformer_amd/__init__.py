@@ -31,6 +31,8 @@ from ._binding import (ACT_GELU, ACT_NONE, EXPORTS, GROUP, LIB_PATH, SVDQError, 
                        svdq_mlp_workspace_bytes, svdq_mx_pack_weights,
                        svdq_mx_quantize_act_down, svdq_mx_lr_gemm,
                        svdq_mx_linear_workspace_bytes, svdq_mx_linear)
+from ._attention import (EXPORTS_ATTENTION, RopeAxes, qkv_norm_rope, rope_axes,  # noqa: F401
+                         rope_tables, svdq_qkv_norm_rope, svdq_rope_tables)
 
 MX_BLOCK = 32   # values per E8M0 scale in the MXFP4 variant
 
