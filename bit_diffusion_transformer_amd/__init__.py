@@ -33,6 +33,9 @@ from ._binding import (ACT_GELU, ACT_NONE, EXPORTS, GROUP, LIB_PATH, SVDQError, 
                        svdq_mx_linear_workspace_bytes, svdq_mx_linear)
 from ._attention import (EXPORTS_ATTENTION, RopeAxes, qkv_norm_rope, rope_axes,  # noqa: F401
                          rope_tables, svdq_qkv_norm_rope, svdq_rope_tables)
+from ._int8 import (EXPORTS_I8, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
+                    i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,
+                    svdq_i8_linear_workspace_bytes, svdq_i8_pack_weights, svdq_i8_quantize_act)
 
 MX_BLOCK = 32   # values per E8M0 scale in the MXFP4 variant
 

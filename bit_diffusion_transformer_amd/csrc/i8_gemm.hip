@@ -1,0 +1,258 @@
+// i8_gemm.hip -- Y = act(diag(sa) (qa qw^T) diag(sw) + bias) on the 8-bit
+// integer matrix instruction (v_mfma_i32_32x32x32_i8).
+//
+// Output tiles are computed transposed, D[n][m] = S[m][n]: the weight codes
+// are the A operand and the activation codes the B operand, so that an output
+// lane holds four consecutive n of one token row.  Both operands are [rows,
+// K] bytes, and a stage of the K loop is 128 of them: one cache line per row.
+// Lines go straight into a ring in LDS (global_load_lds, no registers), each
+// wave reads its fragments with 16-byte LDS reads (XOR-swizzled, no bank
+// conflicts), and the integer sums stay in registers over the whole K loop
+// (exact: K <= 2^17).  The epilogue scales in fp32, adds the bias, applies
+// the activation and rounds once.
+#include "i8_internal.h"
+#include "svdq_device.h"
+
+#include <type_traits>
+
+namespace svdq {
+
+namespace i8 {
+
+constexpr int kRow = 128;        // bytes of a row per stage
+constexpr int kGroupM = 8;       // m tiles per raster group (L2 reuse of weights)
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 32x32 output tile, K = 32 int8 per call: lane l supplies 16 bytes of row /
+// column l % 32, k half l / 32; output element i of lane l is row
+// 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32.
+__device__ __forceinline__ i32x16 mfma_i8_32x32x32(i32x4 a, i32x4 b, i32x16 c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+
+// The 16-byte segment s of a row sits at slot s ^ swz(row): any 8 consecutive
+// rows of one segment touch 8 distinct slots (all banks of a 128-byte pass),
+// any 16 consecutive rows 16 distinct 16-byte groups of 256 bytes.
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// At most `n` vector-memory instructions of this wave in flight, and all its
+// LDS reads returned.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4));
+}
+
+// Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a contiguous
+// range of the tiles, so that tiles sharing operands share its L2.
+__device__ __forceinline__ int64_t xcd_range(int64_t b, int64_t n) {
+    const int64_t x = b & 7, q = n >> 3, r = n & 7;
+    return x * q + (x < r ? x : r) + (b >> 3);
+}
+
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_;          // tokens, output channels
+    static constexpr int WM = WM_, WN = WN_;          // waves along each
+    static constexpr int NBUF = NBUF_;                // stages in the ring
+    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks per wave
+    static constexpr int STAGE = (BM + BN) * kRow;
+    static constexpr int LOADS = (BM + BN) / 8 / WAVES;          // per wave and stage
+    static constexpr int SEGS = NB * 4;               // 16-byte segments of a staged output row
+    static constexpr int OUT = MB * 32 * SEGS * 16;   // a wave's staged output
+    static constexpr int LDS = NBUF * STAGE > WAVES * OUT ? NBUF * STAGE : WAVES * OUT;
+    static_assert(BM == BN && BM % (4 * WAVES) == 0, "half of the waves copy each operand");
+};
+
+template <class T>
+__global__ void __launch_bounds__(T::THREADS)
+i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
+               const int8_t *__restrict__ qw, const float *__restrict__ sw,
+               const uint16_t *__restrict__ bias, int act, int64_t M, int64_t N, int64_t K,
+               uint16_t *__restrict__ Y) {
+    __shared__ __align__(1024) uint8_t lds[T::LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t nbm = (M + T::BM - 1) / T::BM, nbn = (N + T::BN - 1) / T::BN;
+    int64_t m0, n0;
+    {
+        const int64_t id = xcd_range(blockIdx.x, nbm * nbn);
+        const int64_t per = kGroupM * nbn, g = id / per;
+        const int64_t gm = nbm - g * kGroupM < kGroupM ? nbm - g * kGroupM : kGroupM;
+        const int64_t in = id - g * per;
+        m0 = (g * kGroupM + in % gm) * T::BM;
+        n0 = in / gm * T::BN;
+    }
+
+    // Copies of a stage: 1 KB each, 8 rows; lane l carries row l / 8 into slot
+    // l % 8.  Rows past the matrix re-read its last row (never stored).  The
+    // second half of a stage that holds only 64 bytes re-reads the first (its
+    // products are left out).
+    // Waves 0 .. WAVES/2 - 1 carry weight rows (BM == BN), the others token rows.
+    const bool carry_w = wave < T::WAVES / 2;
+    const int8_t *src = carry_w ? qw + n0 * K : qa + m0 * K;
+    uint32_t off[T::LOADS];
+    const int row0 = (wave % (T::WAVES / 2)) * T::LOADS * 8 + lane / 8;
+    {
+        const int64_t left = carry_w ? N - n0 : M - m0;
+#pragma unroll
+        for (int i = 0; i < T::LOADS; ++i) {
+            const int row = row0 + 8 * i;
+            const uint32_t r = row < left ? row : (uint32_t)left - 1;
+            off[i] = r * (uint32_t)K + 16 * ((lane & 7) ^ swz(row));
+        }
+    }
+    const int nf = (int)(K / kRow);                  // whole stages
+    const bool half = (K & 64) != 0;                 // then one of 64 bytes
+    const int ns = nf + (half ? 1 : 0);
+    auto issue = [&](int s) {
+        uint8_t *st = lds + (s % T::NBUF) * T::STAGE + wave * T::LOADS * 1024;
+        const int8_t *g = src + (int64_t)s * kRow;
+        const bool last = s == nf;
+#pragma unroll
+        for (int i = 0; i < T::LOADS; ++i) {
+            uint32_t o = off[i];
+            if (last) {                              // segment seg -> seg % 4
+                const int seg = (lane & 7) ^ swz(row0 + 8 * i);
+                o -= 16 * (seg & 4);
+            }
+            __builtin_amdgcn_global_load_lds(g + o, (lds_void *)(st + i * 1024), 16, 0, 0);
+        }
+    };
+
+    const int wn = wave / T::WM, wm = wave % T::WM;
+    int a_at[4], b_at[4];                            // k step kk: bytes 32 kk .. of a row
+    {
+        const int ar = wn * T::NB * 32 + (lane & 31), br = T::BN + wm * T::MB * 32 + (lane & 31);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int seg = 2 * kk + (lane >> 5);
+            a_at[kk] = ar * kRow + 16 * (seg ^ swz(ar));
+            b_at[kk] = br * kRow + 16 * (seg ^ swz(br));
+        }
+    }
+    i32x16 acc[T::NB][T::MB];
+#pragma unroll
+    for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+        for (int j = 0; j < T::MB; ++j) acc[i][j] = i32x16{};
+
+    auto steps = [&](const uint8_t *st, auto count) {
+#pragma unroll
+        for (int kk = 0; kk < decltype(count)::value; ++kk) {
+            i32x4 a[T::NB], b[T::MB];
+#pragma unroll
+            for (int i = 0; i < T::NB; ++i)
+                a[i] = *reinterpret_cast<const i32x4 *>(st + a_at[kk] + i * 32 * kRow);
+#pragma unroll
+            for (int j = 0; j < T::MB; ++j)
+                b[j] = *reinterpret_cast<const i32x4 *>(st + b_at[kk] + j * 32 * kRow);
+#pragma unroll
+            for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::MB; ++j) acc[i][j] = mfma_i8_32x32x32(a[i], b[j], acc[i][j]);
+        }
+    };
+
+#pragma unroll
+    for (int s = 0; s < T::NBUF - 1; ++s)
+        if (s < ns) issue(s);
+    for (int s = 0; s < nf; ++s) {
+        // stage s has landed when at most the younger stages in flight remain
+        if (s + T::NBUF - 1 <= ns) wait_loads<(T::NBUF - 2) * T::LOADS>();
+        else wait_loads<0>();
+        barrier();
+        if (s + T::NBUF - 1 < ns) issue(s + T::NBUF - 1);
+        steps(lds + (s % T::NBUF) * T::STAGE, std::integral_constant<int, 4>());
+    }
+    if (half) {
+        wait_loads<0>();
+        barrier();
+        steps(lds + (nf % T::NBUF) * T::STAGE, std::integral_constant<int, 2>());
+    }
+    wait_loads<0>();
+    barrier();                                       // the ring becomes the output staging
+
+    // Epilogue: lane l holds, of token column l % 32 of each block, channels
+    // 8 q + 4 (l / 32) .. + 3 for q = 0 .. 3.  The wave stages [token][channel]
+    // bf16 rows in its own part of the LDS and stores them as 16-byte segments.
+    uint8_t *out = lds + wave * T::OUT;
+    const int64_t nw = n0 + wn * T::NB * 32, mw = m0 + wm * T::MB * 32;
+    const int h = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < T::MB; ++j) {
+        const int row = 32 * j + (lane & 31);
+        const int64_t m = mw + row;
+        const float a = m < M ? sa[m] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < T::NB; ++i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t n = nw + 32 * i + 8 * q + 4 * h;
+                f32x4 w = {};
+                u32x2 c = {};
+                if (n < N) {                          // N % 8 == 0: four in or four out
+                    w = *reinterpret_cast<const f32x4 *>(sw + n);
+                    if (bias) c = *reinterpret_cast<const u32x2 *>(bias + n);
+                }
+                const float b[4] = {bf16_lo(c.x), bf16_hi(c.x), bf16_lo(c.y), bf16_hi(c.y)};
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = (float)acc[i][j][4 * q + e] * (a * w[e]) + b[e];
+                    if (act) y[e] = gelu_erf(y[e]);
+                }
+                const int seg = (4 * i + q) ^ (row & (T::SEGS - 1));
+                *reinterpret_cast<u32x2 *>(out + (row * T::SEGS + seg) * 16 + 8 * h) =
+                    u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int ROWS = 64 / T::SEGS;               // rows per store instruction
+#pragma unroll
+    for (int it = 0; it < T::MB * 32 / ROWS; ++it) {
+        const int row = it * ROWS + lane / T::SEGS, sl = lane % T::SEGS;
+        const u32x4 y = *reinterpret_cast<const u32x4 *>(out + (row * T::SEGS + (sl ^ (row & (T::SEGS - 1)))) * 16);
+        const int64_t m = mw + row, n = nw + 8 * sl;
+        if (m < M && n < N) *reinterpret_cast<u32x4 *>(Y + m * N + n) = y;
+    }
+}
+
+typedef Tile<256, 256, 4, 2, 2> Big;
+typedef Tile<128, 128, 2, 2, 2> Mid;
+typedef Tile<64, 64, 2, 2, 4> Small;
+
+template <class T>
+int64_t tiles(int64_t M, int64_t N) {
+    return (M + T::BM - 1) / T::BM * ((N + T::BN - 1) / T::BN);
+}
+
+}  // namespace i8
+
+using namespace i8;
+
+int64_t i8_gemm_groups(int64_t M, int64_t N) { return tiles<Small>(M, N); }
+size_t i8_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
+                          const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,
+                          uint16_t *Y, void *workspace, hipStream_t stream) {
+    (void)workspace;
+    const int64_t cus = wg_slots() / 2;
+    if (tiles<Big>(M, N) >= cus)
+        i8_gemm_kernel<Big><<<(unsigned)tiles<Big>(M, N), Big::THREADS, 0, stream>>>(
+            qa, sa, qw, sw, bias, act, M, N, K, Y);
+    else if (tiles<Mid>(M, N) >= cus)
+        i8_gemm_kernel<Mid><<<(unsigned)tiles<Mid>(M, N), Mid::THREADS, 0, stream>>>(
+            qa, sa, qw, sw, bias, act, M, N, K, Y);
+    else
+        i8_gemm_kernel<Small><<<(unsigned)tiles<Small>(M, N), Small::THREADS, 0, stream>>>(
+            qa, sa, qw, sw, bias, act, M, N, K, Y);
+    return hipGetLastError();
+}
+
+}  // namespace svdq

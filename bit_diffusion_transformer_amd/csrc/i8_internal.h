@@ -1,0 +1,22 @@
+// i8_internal.h -- launchers of the 8-bit integer linear (internal; not part
+// of the ABI).
+#pragma once
+
+#include "svdq_i8.h"
+#include "svdq_internal.h"
+
+namespace svdq {
+
+// X bf16 [M, K] (smoothed by 1 / lambda unless lambda is null) or, with
+// `fp32`, fp32 rows without smoothing -> codes [M, K] and scales [M]
+hipError_t launch_i8_quantize(const void *X, bool fp32, const float *lambda, int64_t M, int64_t K,
+                              int8_t *q, float *s, hipStream_t stream);
+int64_t i8_quantize_groups(int64_t M, int64_t K);   // workgroups of 256
+
+hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
+                          const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,
+                          uint16_t *Y, void *workspace, hipStream_t stream);
+int64_t i8_gemm_groups(int64_t M, int64_t N);       // workgroups at most, of 512
+size_t i8_gemm_workspace(int64_t M, int64_t N, int64_t K);
+
+}  // namespace svdq
