@@ -31,8 +31,12 @@ from ._binding import (ACT_GELU, ACT_NONE, EXPORTS, GROUP, LIB_PATH, SVDQError, 
                        svdq_mlp_workspace_bytes, svdq_mx_pack_weights,
                        svdq_mx_quantize_act_down, svdq_mx_lr_gemm,
                        svdq_mx_linear_workspace_bytes, svdq_mx_linear)
-from ._attention import (EXPORTS_ATTENTION, RopeAxes, qkv_norm_rope, rope_axes,  # noqa: F401
-                         rope_tables, svdq_qkv_norm_rope, svdq_rope_tables)
+from ._attention import (EXPORTS_ATTENTION, AttentionShape, KEY_BLOCK, QUERY_BLOCK,  # noqa: F401
+                         RopeAxes, block_attention, qkv_norm_rope, rope_axes, rope_tables,
+                         select_blocks, sparse_attention, svdq_block_attention,
+                         svdq_block_attention_workspace_bytes, svdq_qkv_norm_rope,
+                         svdq_rope_tables, svdq_select_blocks, svdq_select_blocks_workspace_bytes,
+                         svdq_sparse_attention, svdq_sparse_attention_workspace_bytes)
 from ._int8 import (EXPORTS_I8, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
                     i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,
                     svdq_i8_linear_workspace_bytes, svdq_i8_pack_weights, svdq_i8_quantize_act)

@@ -8,10 +8,11 @@ from typing import Optional, Sequence
 import torch
 
 from ._binding import QkvEpilogue, qkv_epilogue
-from ._tensors import (BF16, Entries, F32, I32T, I64, P, expect, on, one_device, ptr,
-                       stream_ptr)
+from ._tensors import (BF16, Entries, F32, F32T, I32, I32T, I64, P, SZ, expect, on, one_device,
+                       ptr, scratch, stream_ptr)
 
 ROPE_MAX_AXES = 4
+QUERY_BLOCK, KEY_BLOCK = 128, 64
 
 
 class RopeAxes(ctypes.Structure):
@@ -20,9 +21,23 @@ class RopeAxes(ctypes.Structure):
                 ("theta", ctypes.c_double * ROPE_MAX_AXES)]
 
 
+class AttentionShape(ctypes.Structure):
+    """struct svdq_attention_shape of include/svdq_attention.h."""
+    _fields_ = [("batch", ctypes.c_int64), ("seq_q", ctypes.c_int64), ("seq_k", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("keep", ctypes.c_int32), ("first", ctypes.c_int32)]
+
+
+_SHAPE = ctypes.POINTER(AttentionShape)
 _entries = Entries({
     "svdq_rope_tables": ([P, I64, ctypes.POINTER(RopeAxes), P, P, P], I32T),
     "svdq_qkv_norm_rope": ([P, I64, ctypes.POINTER(QkvEpilogue), P], I32T),
+    "svdq_select_blocks_workspace_bytes": ([_SHAPE], SZ),
+    "svdq_select_blocks": ([P, P, P, _SHAPE, P, P, SZ, P], I32T),
+    "svdq_block_attention_workspace_bytes": ([_SHAPE], SZ),
+    "svdq_block_attention": ([P, P, P, P, _SHAPE, F32T, P, P, P, SZ, P], I32T),
+    "svdq_sparse_attention_workspace_bytes": ([_SHAPE], SZ),
+    "svdq_sparse_attention": ([P, P, P, P, _SHAPE, F32T, P, P, P, SZ, P], I32T),
 })
 # Every symbol declared in include/svdq_attention.h.
 EXPORTS_ATTENTION = _entries.names()
@@ -37,6 +52,38 @@ def svdq_rope_tables(pos, S, axes: RopeAxes, cos_t, sin_t, stream=None):
 
 def svdq_qkv_norm_rope(qkv, M, epi: QkvEpilogue, stream=None):
     _entries.call("svdq_qkv_norm_rope", ptr(qkv), M, ctypes.byref(epi), stream_ptr(stream))
+
+
+def svdq_select_blocks_workspace_bytes(shape: AttentionShape) -> int:
+    return int(_entries["svdq_select_blocks_workspace_bytes"](ctypes.byref(shape)))
+
+
+def svdq_select_blocks(q, k, kv_len, shape: AttentionShape, blocks, workspace, ws_bytes,
+                       stream=None):
+    _entries.call("svdq_select_blocks", ptr(q), ptr(k), ptr(kv_len), ctypes.byref(shape),
+                  ptr(blocks), ptr(workspace), ws_bytes, stream_ptr(stream))
+
+
+def svdq_block_attention_workspace_bytes(shape: AttentionShape) -> int:
+    return int(_entries["svdq_block_attention_workspace_bytes"](ctypes.byref(shape)))
+
+
+def svdq_block_attention(q, k, v, kv_len, shape: AttentionShape, scale, blocks, out, workspace,
+                         ws_bytes, stream=None):
+    _entries.call("svdq_block_attention", ptr(q), ptr(k), ptr(v), ptr(kv_len),
+                  ctypes.byref(shape), scale, ptr(blocks), ptr(out), ptr(workspace), ws_bytes,
+                  stream_ptr(stream))
+
+
+def svdq_sparse_attention_workspace_bytes(shape: AttentionShape) -> int:
+    return int(_entries["svdq_sparse_attention_workspace_bytes"](ctypes.byref(shape)))
+
+
+def svdq_sparse_attention(q, k, v, kv_len, shape: AttentionShape, scale, blocks, out, workspace,
+                          ws_bytes, stream=None):
+    _entries.call("svdq_sparse_attention", ptr(q), ptr(k), ptr(v), ptr(kv_len),
+                  ctypes.byref(shape), scale, ptr(blocks), ptr(out), ptr(workspace), ws_bytes,
+                  stream_ptr(stream))
 
 
 # ------------------------------------------------------------- tensor level
@@ -90,3 +137,67 @@ def qkv_norm_rope(qkv: torch.Tensor, heads: int, head_dim: int, seq: int, gamma_
     with on(dev):
         svdq_qkv_norm_rope(qkv, M, epi)
     return Q, K, V
+
+
+def _shape(q, k, kv_len, keep, first) -> AttentionShape:
+    B, H, Sq, D = expect(q, "q", BF16, (None, None, None, None)).shape
+    _, G, Sk, _ = expect(k, "k", BF16, (B, None, None, D)).shape
+    if kv_len is not None:
+        expect(kv_len, "kv_len", I32, (B,))
+    return AttentionShape(B, Sq, Sk, H, G, D, keep, first)
+
+
+def _lists(s: AttentionShape):
+    return (s.batch, s.heads, -(-s.seq_q // QUERY_BLOCK), s.keep)
+
+
+def select_blocks(q, k, keep: int, first: int = 0, kv_len: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Q bf16 [B, H, Sq, D], K bf16 [B, G, Sk, D] -> int32 [B, H, ceil(Sq/128), keep]: for each
+    block of 128 queries the `keep` blocks of 64 keys whose mean has the highest product with
+    the queries' mean (the first `first` always), ascending, -1 behind the last."""
+    s = _shape(q, k, kv_len, keep, first)
+    dev = one_device(q=q, k=k, kv_len=kv_len)
+    blocks = torch.empty(_lists(s), dtype=torch.int32, device=dev)
+    need = svdq_select_blocks_workspace_bytes(s)
+    ws = scratch(workspace, need, dev)
+    with on(dev):
+        svdq_select_blocks(q, k, kv_len, s, blocks, ws, need)
+    return blocks
+
+
+def block_attention(q, k, v, blocks, scale: Optional[float] = None,
+                    kv_len: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each block of 128 queries over its list of key blocks (int32 [B, H,
+    ceil(Sq/128), keep]) -> bf16 [B, Sq, H, D]; scale None: D^-1/2."""
+    expect(blocks, "blocks", I32, (None, None, None, None))
+    s = _shape(q, k, kv_len, blocks.shape[3], 0)
+    expect(v, "v", BF16, tuple(k.shape))
+    expect(blocks, "blocks", I32, _lists(s))
+    dev = one_device(q=q, k=k, v=v, blocks=blocks, kv_len=kv_len)
+    out = torch.empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16, device=dev)
+    need = svdq_block_attention_workspace_bytes(s)
+    ws = scratch(workspace, need, dev)
+    with on(dev):
+        svdq_block_attention(q, k, v, kv_len, s, s.head_dim ** -0.5 if scale is None else scale,
+                             blocks, out, ws, need)
+    return out
+
+
+def sparse_attention(q, k, v, keep: int, first: int = 0, scale: Optional[float] = None,
+                     kv_len: Optional[torch.Tensor] = None, return_blocks: bool = False,
+                     workspace: Optional[torch.Tensor] = None):
+    """select_blocks and block_attention in one call -> bf16 [B, Sq, H, D] (with the lists
+    if return_blocks)."""
+    s = _shape(q, k, kv_len, keep, first)
+    expect(v, "v", BF16, tuple(k.shape))
+    dev = one_device(q=q, k=k, v=v, kv_len=kv_len)
+    out = torch.empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16, device=dev)
+    blocks = torch.empty(_lists(s), dtype=torch.int32, device=dev) if return_blocks else None
+    need = svdq_sparse_attention_workspace_bytes(s)
+    ws = scratch(workspace, need, dev)
+    with on(dev):
+        svdq_sparse_attention(q, k, v, kv_len, s, s.head_dim ** -0.5 if scale is None else scale,
+                              blocks, out, ws, need)
+    return (out, blocks) if return_blocks else out

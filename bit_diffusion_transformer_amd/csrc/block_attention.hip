@@ -1,0 +1,381 @@
+// block_attention.hip -- attention of blocks of 128 queries over lists of key
+// blocks of 64, on the bf16 matrix instruction (v_mfma_f32_32x32x16_bf16).
+//
+// One workgroup of four waves per query block and head, 32 queries a wave.
+// Scores are computed transposed, S^T = K Q^T, so that a lane holds the scores
+// of one query (column l % 32, half of the block's keys; lane l ^ 32 the other
+// half): the running maximum and sum of the softmax stay within the lane but
+// for one exchange, and the weights P^T come out in the lane layout that the
+// second product, O^T = V^T P^T, takes as its operand, without a pass through
+// LDS (its order of keys within a step is that of the score tile's rows, and
+// the V operand is read in the same order).  K and V blocks go from global
+// memory straight into LDS (two buffers, the next block's copies in flight
+// while the current one is used); K is read in 16-byte pieces, V through the
+// transposing 8-byte LDS read.
+#include "attention_internal.h"
+#include "svdq_device.h"
+
+namespace svdq {
+
+namespace attn {
+
+constexpr int kQB = SVDQ_QUERY_BLOCK, kKB = SVDQ_KEY_BLOCK;
+constexpr int kMaxList = SVDQ_MAX_KEYS / SVDQ_KEY_BLOCK;
+
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// Every vector-memory instruction of this wave done and its LDS reads returned.
+__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x7 << 4); }
+
+__device__ __forceinline__ float max_both_halves(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float sum_both_halves(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// LDS layout of a K or V block: rows of D values, 16-byte segments XORed by a
+// function of the row.  K: eight (sixteen) consecutive rows of one segment hit
+// different banks.  V: four consecutive rows of two neighbouring segments do
+// (what a 16-lane group of the transposing read touches).
+template <int D>
+__device__ __forceinline__ int swz_k(int row) {
+    return D == 128 ? row & 15 : (row & 7) ^ ((row >> 3) & 1);
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int row) {
+    return D == 128 ? 2 * (row & 7) : 2 * (row & 3);
+}
+
+// Transposing LDS read: within each 16 lanes, lane i supplies 8 bytes (4 columns)
+// of row i / 4 and receives column i of the four rows.
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t *p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+}
+
+template <int D>
+struct Lds {
+    static constexpr int TILE = kKB * D * 2;      // bytes of a K or V block
+    uint8_t k[2][TILE];
+    uint8_t v[2][TILE];
+    uint16_t list[kMaxList];
+    int count;
+};
+
+// The list's usable entries, in order: not negative, below `valid`, above every
+// entry before them.  By the first wave.
+__device__ __forceinline__ void read_list(const int32_t *__restrict__ blocks, int keep, int valid,
+                                          uint16_t *list, int *count) {
+    const int lane = threadIdx.x & 63;
+    int n = 0, top = -1;
+    for (int i0 = 0; i0 < keep; i0 += 64) {
+        const int e = i0 + lane < keep ? blocks[i0 + lane] : -1;
+        int best = e;                              // inclusive running maximum
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(best, d);
+            if (lane >= d) best = o > best ? o : best;
+        }
+        int before = __shfl_up(best, 1);
+        before = lane == 0 || before < top ? top : before;
+        const bool take = e >= 0 && e < valid && e > before;
+        const uint64_t taken = __ballot(take);
+        if (take) list[n + __popcll(taken & ((1ull << lane) - 1))] = (uint16_t)e;
+        n += __popcll(taken);
+        const int last = __shfl(best, 63);
+        top = last > top ? last : top;
+    }
+    if (lane == 0) *count = n;
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(256, 2)
+block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
+                       const uint16_t *__restrict__ v, const int32_t *__restrict__ kv_len,
+                       AttnShape a, float scale_log2, const int32_t *__restrict__ blocks,
+                       uint16_t *__restrict__ out, int splits, float *__restrict__ part,
+                       float *__restrict__ stat) {
+    constexpr int DB = D / 32, DK = D / 16;        // 32-wide blocks and 16-wide steps of D
+    constexpr int RPT = 512 / D;                   // rows per 1 KB copy
+    constexpr int SEGS = D / 8;                    // 16-byte segments of a row
+    constexpr int COPIES = kKB / RPT / 4;          // copies per wave, K and V each
+    __shared__ __align__(1024) Lds<D> lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h2 = lane >> 5, col = lane & 31;
+
+    // Consecutive workgroups go to the 8 XCDs in turn: each gets a contiguous
+    // range of the query blocks, whose lists share key blocks in its L2.
+    int64_t id;
+    {
+        const int64_t n = a.planes_q * a.nq * (SPLIT ? splits : 1);
+        const int64_t x = blockIdx.x & 7, per = n >> 3, r = n & 7;
+        id = x * per + (x < r ? x : r) + (blockIdx.x >> 3);
+    }
+    const int piece = SPLIT ? (int)(id % splits) : 0;
+    if (SPLIT) id /= splits;
+    const int64_t plane = id / a.nq, qi = id - plane * a.nq;
+    const int64_t b = plane / a.H, h = plane - b * a.H;
+    const int64_t kplane = b * a.G + h / (a.H / a.G);
+    int len = (int)a.seq_k;                        // <= 2^18
+    if (kv_len) {
+        const int n = kv_len[b];
+        len = n < 0 ? 0 : n > len ? len : n;
+    }
+    if (wave == 0)
+        read_list(blocks + id * a.keep, a.keep, (len + kKB - 1) / kKB, lds.list, &lds.count);
+    __syncthreads();
+    int first = 0, last = lds.count;
+    if (SPLIT) {
+        const int n = last;
+        first = (int)((int64_t)n * piece / splits);
+        last = (int)((int64_t)n * (piece + 1) / splits);
+    }
+
+    const uint8_t *kb = reinterpret_cast<const uint8_t *>(k + kplane * a.seq_k * D);
+    const uint8_t *vb = reinterpret_cast<const uint8_t *>(v + kplane * a.seq_k * D);
+    // Rows at or past the sequence's length re-read its last valid row: their
+    // scores are masked, and their weights are zeros times finite values.
+    auto issue = [&](int i) {
+        const int buf = (i - first) & 1, n0 = (int)lds.list[i] * kKB;
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c) {
+            const int row = (wave * COPIES + c) * RPT + lane / SEGS, slot = lane % SEGS;
+            const int n = n0 + row < len ? n0 + row : len - 1;
+            const uint32_t at = (uint32_t)n * (D * 2);
+            const int dst = (wave * COPIES + c) * 1024;
+            copy16_to_lds(kb + at + 16 * (slot ^ swz_k<D>(row)), lds.k[buf] + dst);
+            copy16_to_lds(vb + at + 16 * (slot ^ swz_v<D>(row)), lds.v[buf] + dst);
+        }
+    };
+    if (first < last) issue(first);
+
+    // This lane's query, rows past the last re-reading it (never stored).
+    const int64_t row0 = qi * kQB + wave * 32;
+    const bool active = row0 < a.seq_q;            // uniform over the wave
+    const int64_t qrow = row0 + col < a.seq_q ? row0 + col : a.seq_q - 1;
+    u32x4 qf[DK];
+    {
+        const uint16_t *p = q + (plane * a.seq_q + qrow) * D + 8 * h2;
+#pragma unroll
+        for (int s = 0; s < DK; ++s) qf[s] = *reinterpret_cast<const u32x4 *>(p + 16 * s);
+    }
+
+    // LDS offsets: K row `col`, segment 2 s + h2 of step s; V: lane i of a
+    // 16-lane group supplies row i / 4 of four keys, 4 columns from 4 (i % 4) of
+    // the group's 16, and gets column i of the four rows.
+    int v_row, v_sub;
+    {
+        const int i = lane & 15;
+        v_row = 4 * h2 + (i >> 2);
+        v_sub = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);     // segment within a 32-wide block
+    }
+    const int v_byte = 8 * (lane & 1);
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    for (int i = first; i < last; ++i) {
+        const int buf = (i - first) & 1, n0 = (int)lds.list[i] * kKB;
+        wait_all();
+        barrier();
+        if (i + 1 < last) issue(i + 1);
+        if (!active) continue;
+        f32x16 s[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+        for (int t = 0; t < DK; ++t)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const int row = 32 * kk + col;
+                const u32x4 kf = *reinterpret_cast<const u32x4 *>(
+                    lds.k[buf] + row * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(row)));
+                s[kk] = mfma_bf16_32x32x16(kf, qf[t], s[kk]);
+            }
+        if (n0 + kKB > len) {                      // the sequence ends in this block
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int n = n0 + 32 * kk + 8 * (e / 4) + 4 * h2 + e % 4;
+                    if (n >= len) s[kk][e] = -__builtin_inff();
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+        top = max_both_halves(top);
+        // The running maximum moves only when a score passes it by more than 8
+        // in the exponent of two: the weights stay below 2^8, and most blocks
+        // leave the sums as they are.
+        if (__any((top - m) * scale_log2 > 8.0f)) {
+            const float m1 = fmaxf(m, top);
+            const float f = __builtin_amdgcn_exp2f((m - m1) * scale_log2);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] *= f;
+        }
+        const float off = m * scale_log2;
+        u32x4 p[2][2];                             // [kk][step of 16 keys]: weights in bf16
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[kk][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kk][e], scale_log2, -off));
+                l += s[kk][e];
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    p[kk][t][w] = pack_bf16x2(s[kk][8 * t + 2 * w], s[kk][8 * t + 2 * w + 1]);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    u32x4 vf;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {  // keys 0 .. 3 and 8 .. 11 past 4 h2
+                        const int row = 32 * kk + 16 * t + 8 * u + v_row;
+                        const int at = row * (D * 2) + 16 * ((4 * d + v_sub) ^ swz_v<D>(row)) + v_byte;
+                        const u32x2 y = read_transposed(lds.v[buf] + at);
+                        vf[2 * u] = y.x;
+                        vf[2 * u + 1] = y.y;
+                    }
+                    o[d] = mfma_bf16_32x32x16(vf, p[kk][t], o[d]);
+                }
+    }
+    if (!active) return;
+
+    l = sum_both_halves(l);
+    if (SPLIT) {
+        // unnormalized sums fp32 [piece][B H Sq][D], maximum and sum [piece][B H Sq][2]
+        if (row0 + col < a.seq_q) {
+            const int64_t at = (int64_t)piece * a.planes_q * a.seq_q + plane * a.seq_q + row0 + col;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<f32x4 *>(part + at * D + 32 * d + 8 * e + 4 * h2) =
+                        f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+            if (h2 == 0) {
+                stat[2 * at] = m;
+                stat[2 * at + 1] = l;
+            }
+        }
+        return;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    // A lane holds d = 32 db + 8 e + 4 h2 + (0 .. 3) of its query; the swap of
+    // the lane halves gives each eight consecutive ones: 16-byte stores.
+    uint16_t *dst = out + ((b * a.seq_q + row0 + col) * a.H + h) * D;
+    const bool in = row0 + col < a.seq_q;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            u32x2 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                x[u] = u32x2{pack_bf16x2(o[d][4 * (e + u)] * inv, o[d][4 * (e + u) + 1] * inv),
+                             pack_bf16x2(o[d][4 * (e + u) + 2] * inv, o[d][4 * (e + u) + 3] * inv)};
+            const auto s0 = __builtin_amdgcn_permlane32_swap(x[0].x, x[1].x, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(x[0].y, x[1].y, false, false);
+            if (in)
+                *reinterpret_cast<u32x4 *>(dst + 32 * d + 8 * (e + h2)) =
+                    u32x4{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+        }
+}
+
+// Joins the pieces of each row: the largest maximum, weights 2^(m_i - m) on sums
+// and results.  D / 4 lanes per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+join_kernel(const float *__restrict__ part, const float *__restrict__ stat, AttnShape a, int splits,
+            float scale_log2, uint16_t *__restrict__ out) {
+    constexpr int LANES = D / 4;
+    const int64_t rows = a.planes_q * a.seq_q;
+    const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+    const int c = threadIdx.x % LANES;
+    if (row >= rows) return;
+    float m = -__builtin_inff();
+    for (int i = 0; i < splits; ++i) m = fmaxf(m, stat[2 * (i * rows + row)]);
+    float l = 0.0f;
+    f32x4 o = {};
+    if (m > -__builtin_inff()) {
+        for (int i = 0; i < splits; ++i) {
+            const float f = __builtin_amdgcn_exp2f((stat[2 * (i * rows + row)] - m) * scale_log2);
+            l += f * stat[2 * (i * rows + row) + 1];
+            o += f * *reinterpret_cast<const f32x4 *>(part + (i * rows + row) * D + 4 * c);
+        }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t plane = row / a.seq_q, s = row - plane * a.seq_q;
+    const int64_t b = plane / a.H, h = plane - b * a.H;
+    *reinterpret_cast<u32x2 *>(out + ((b * a.seq_q + s) * a.H + h) * D + 4 * c) =
+        u32x2{pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)};
+}
+
+template <int D>
+hipError_t launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kv_len,
+                  const AttnShape &a, float scale, const int32_t *blocks, uint16_t *out, void *ws,
+                  hipStream_t stream) {
+    const float c = scale * 1.4426950408889634f;
+    const int splits = attention_splits(a);
+    const unsigned grid = (unsigned)(a.planes_q * a.nq * splits);
+    if (splits == 1) {
+        block_attention_kernel<D, false><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, out,
+                                                                   1, nullptr, nullptr);
+        return hipGetLastError();
+    }
+    const int64_t rows = a.planes_q * a.seq_q;
+    float *part = static_cast<float *>(ws), *stat = part + rows * splits * D;
+    block_attention_kernel<D, true><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, out,
+                                                              splits, part, stat);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    constexpr int per = 256 / (D / 4);
+    join_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(part, stat, a, splits, c, out);
+    return hipGetLastError();
+}
+
+}  // namespace attn
+
+// Few query blocks: the lists are shared among workgroups until there are
+// about two per compute unit, four key blocks a piece at least.
+int attention_splits(const AttnShape &a) {
+    const int64_t wgs = a.planes_q * a.nq;
+    if (wgs >= 256 || wgs == 0) return 1;
+    const int64_t taken = a.keep < a.nk ? a.keep : a.nk;
+    int64_t s = (512 + wgs - 1) / wgs;
+    if (s > taken / 4) s = taken / 4;
+    if (s > 32) s = 32;
+    return s < 1 ? 1 : (int)s;
+}
+
+size_t attention_workspace(const AttnShape &a) {
+    const int s = attention_splits(a);
+    return s == 1 ? 0 : align256((size_t)(a.planes_q * a.seq_q) * s * (a.D + 2) * 4);
+}
+
+hipError_t launch_block_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                  const int32_t *kv_len, const AttnShape &a, float scale,
+                                  const int32_t *blocks, uint16_t *out, void *ws,
+                                  hipStream_t stream) {
+    return a.D == 64 ? attn::launch<64>(q, k, v, kv_len, a, scale, blocks, out, ws, stream)
+                     : attn::launch<128>(q, k, v, kv_len, a, scale, blocks, out, ws, stream);
+}
+
+}  // namespace svdq

@@ -23,7 +23,6 @@ constexpr int kRow = 128;        // bytes of a row per stage
 constexpr int kGroupM = 8;       // m tiles per raster group (L2 reuse of weights)
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 // 32x32 output tile, K = 32 int8 per call: lane l supplies 16 bytes of row /
 // column l % 32, k half l / 32; output element i of lane l is row
@@ -119,7 +118,7 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
                 const int seg = (lane & 7) ^ swz(row0 + 8 * i);
                 o -= 16 * (seg & 4);
             }
-            __builtin_amdgcn_global_load_lds(g + o, (lds_void *)(st + i * 1024), 16, 0, 0);
+            copy16_to_lds(g + o, st + i * 1024);
         }
     };
 

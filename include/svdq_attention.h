@@ -24,6 +24,9 @@ extern "C" {
 
 #define SVDQ_ROPE_MAX_AXES 4
 #define SVDQ_ROPE_MAX_DIM 256   /* largest head_dim of the tables */
+#define SVDQ_QUERY_BLOCK 128    /* query rows that share one list of key blocks */
+#define SVDQ_KEY_BLOCK 64       /* keys per block */
+#define SVDQ_MAX_KEYS (1 << 18) /* largest seq_k of the sparse attention */
 
 /*
  * How a head's dimension is divided among the position axes (e.g. time,
@@ -61,6 +64,83 @@ int32_t svdq_rope_tables(const float *pos, int64_t S, const svdq_rope_axes *axes
  */
 int32_t svdq_qkv_norm_rope(const uint16_t *qkv, int64_t M, const svdq_qkv_epilogue *epi,
                            void *stream);
+
+/* ------------------------------------------------------------------
+ * Block-sparse attention.  The queries of a head are taken in blocks of 128
+ * rows, the keys in blocks of 64.  The score of query block i and key block j
+ * is the product of the two blocks' means (over the query rows that exist,
+ * and over the keys below kv_len); query block i attends to the `keep` key
+ * blocks with the highest scores:
+ *   O[m] = sum_n p[m][n] v[n],  p = softmax over the keys n of those blocks
+ *          of scale q[m] . k[n].
+ * Keys at or past a sequence's kv_len take no part, whatever they hold.  A
+ * query block without any key gives rows of zeros.
+ * ------------------------------------------------------------------ */
+typedef struct svdq_attention_shape {
+    int64_t batch;      /* B >= 0 (0: no-op) */
+    int64_t seq_q;      /* Sq >= 0 (0: no-op) */
+    int64_t seq_k;      /* Sk, 1 .. SVDQ_MAX_KEYS */
+    int32_t heads;      /* H >= 1 */
+    int32_t kv_heads;   /* G >= 1, H % G == 0: head h reads key head h / (H / G) */
+    int32_t head_dim;   /* D: 64 or 128 */
+    int32_t keep;       /* key blocks per query block, 1 .. SVDQ_MAX_KEYS / 64 */
+    int32_t first;      /* 0 .. keep: the first `first` key blocks are always taken (and count) */
+} svdq_attention_shape;
+
+/* Workspace of svdq_select_blocks: the blocks' means. */
+size_t svdq_select_blocks_workspace_bytes(const svdq_attention_shape *shape);
+
+/*
+ * The lists of key blocks.
+ *   q       device bf16 [B, H, Sq, D]
+ *   k       device bf16 [B, G, Sk, D]
+ *   kv_len  device int32 [B] valid keys of each sequence (clamped to 0 .. Sk),
+ *           or NULL: all Sk
+ *   blocks  device int32 [B, H, ceil(Sq/128), keep] (out): the block numbers
+ *           in ascending order, -1 behind the last one where fewer than
+ *           `keep` blocks hold a valid key
+ * Means and scores are taken in 64 bits; equal scores go to the lower block
+ * number.  q and the valid keys must be finite (otherwise which blocks are
+ * taken is unspecified).
+ */
+int32_t svdq_select_blocks(const uint16_t *q, const uint16_t *k, const int32_t *kv_len,
+                           const svdq_attention_shape *shape, int32_t *blocks, void *workspace,
+                           size_t ws_bytes, void *stream);
+
+/* Workspace of svdq_block_attention: partial results where few query blocks
+ * are split over their keys (0 elsewhere). */
+size_t svdq_block_attention_workspace_bytes(const svdq_attention_shape *shape);
+
+/*
+ * Attention over given lists (shape's `first` is not read).
+ *   v       device bf16 [B, G, Sk, D]
+ *   scale   finite and > 0 (usually D^-1/2)
+ *   blocks  device int32 [B, H, ceil(Sq/128), keep]: an entry that is
+ *           negative, past the last block with a valid key, or not above
+ *           every entry before it in its list is passed over, so a block
+ *           named twice counts once
+ *   out     device bf16 [B, Sq, H, D] (out): the rows [M, H D] of the output
+ *           projection
+ * Products in bf16 with fp32 sums; the softmax in fp32 with the running
+ * maximum and sum; its weights are rounded once to bf16 for the product with
+ * v; one rounding of the result to bf16.
+ */
+int32_t svdq_block_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                             const int32_t *kv_len, const svdq_attention_shape *shape,
+                             float scale, const int32_t *blocks, uint16_t *out, void *workspace,
+                             size_t ws_bytes, void *stream);
+
+/* Workspace of svdq_sparse_attention (both steps and the lists). */
+size_t svdq_sparse_attention_workspace_bytes(const svdq_attention_shape *shape);
+
+/*
+ * svdq_select_blocks then svdq_block_attention on one stream.  blocks: the
+ * lists (out), or NULL: they stay in the workspace.
+ */
+int32_t svdq_sparse_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                              const int32_t *kv_len, const svdq_attention_shape *shape,
+                              float scale, int32_t *blocks, uint16_t *out, void *workspace,
+                              size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

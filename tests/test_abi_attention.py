@@ -148,3 +148,110 @@ def test_tensor_functions_refuse_bad_tensors():
         bdt.qkv_norm_rope(qkv[:7], 2, 64, 4, None, None, 1e-6, t, t)
     with pytest.raises(TypeError):
         bdt.qkv_norm_rope(qkv.float(), 2, 64, 4, None, None, 1e-6, t, t)
+
+
+# ---------------------------------------------------------------- sparse attention
+
+def test_attention_shape_layout_matches_header(tmp_path):
+    _layout(tmp_path, "svdq_attention_shape", bdt.AttentionShape)
+
+
+def _shape(**kw):
+    s = dict(batch=2, seq_q=200, seq_k=300, heads=4, kv_heads=2, head_dim=128, keep=3, first=1)
+    s.update(kw)
+    return bdt.AttentionShape(**s)
+
+
+def _select(fn, shape=None, q=A, k=A, kv_len=0, blocks=A, ws=A, ws_bytes=1 << 40):
+    return fn["svdq_select_blocks"](P(q), P(k), P(kv_len), ctypes.byref(shape or _shape()),
+                                    P(blocks), P(ws), ws_bytes, None)
+
+
+def _block(fn, shape=None, q=A, k=A, v=A, kv_len=0, scale=0.1, blocks=A, out=A, ws=A,
+           ws_bytes=1 << 40):
+    return fn["svdq_block_attention"](P(q), P(k), P(v), P(kv_len), ctypes.byref(shape or _shape()),
+                                      scale, P(blocks), P(out), P(ws), ws_bytes, None)
+
+
+def _sparse(fn, shape=None, q=A, k=A, v=A, kv_len=0, scale=0.1, blocks=0, out=A, ws=A,
+            ws_bytes=1 << 40):
+    return fn["svdq_sparse_attention"](P(q), P(k), P(v), P(kv_len), ctypes.byref(shape or _shape()),
+                                       scale, P(blocks), P(out), P(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), INVALID), (dict(seq_q=-1), INVALID), (dict(batch=(1 << 28) + 1), SHAPE),
+    (dict(seq_k=0), SHAPE), (dict(seq_k=-5), SHAPE), (dict(seq_k=(1 << 18) + 1), SHAPE),
+    (dict(heads=0), INVALID), (dict(heads=-4), INVALID), (dict(kv_heads=0), SHAPE),
+    (dict(kv_heads=3), SHAPE), (dict(kv_heads=-2), SHAPE), (dict(head_dim=96), SHAPE),
+    (dict(head_dim=256), SHAPE), (dict(keep=0), SHAPE), (dict(keep=4097), SHAPE),
+    (dict(first=-1), INVALID), (dict(first=4), INVALID),
+    (dict(batch=1 << 27, heads=4), SHAPE), (dict(batch=1 << 10, heads=1 << 10, seq_q=1 << 20), SHAPE),
+    (dict(batch=1 << 20, seq_k=1 << 18), SHAPE),
+])
+def test_sparse_attention_rejects_shapes(fn, kw, code):
+    for call in (_select, _block, _sparse):
+        assert call(fn, _shape(**kw)) == code
+        assert last()
+    for size in ("select_blocks", "block_attention", "sparse_attention"):
+        assert fn["svdq_%s_workspace_bytes" % size](ctypes.byref(_shape(**kw))) == 0
+
+
+@pytest.mark.parametrize("call,kw,code", [
+    (_select, dict(q=0), INVALID), (_select, dict(k=U), MISALIGNED), (_select, dict(kv_len=U), MISALIGNED),
+    (_select, dict(blocks=0), INVALID), (_select, dict(ws=0), INVALID), (_select, dict(ws_bytes=8), WS_SMALL),
+    (_block, dict(q=U), MISALIGNED), (_block, dict(k=0), INVALID), (_block, dict(v=0), INVALID),
+    (_block, dict(blocks=U), MISALIGNED), (_block, dict(out=0), INVALID), (_block, dict(kv_len=U), MISALIGNED),
+    (_block, dict(scale=0.0), INVALID), (_block, dict(scale=-1.0), INVALID),
+    (_block, dict(scale=float("inf")), INVALID), (_block, dict(scale=float("nan")), INVALID),
+    (_sparse, dict(q=0), INVALID), (_sparse, dict(v=U), MISALIGNED), (_sparse, dict(out=U), MISALIGNED),
+    (_sparse, dict(blocks=U), MISALIGNED), (_sparse, dict(scale=float("nan")), INVALID),
+    (_sparse, dict(ws=U), MISALIGNED), (_sparse, dict(ws_bytes=8), WS_SMALL),
+])
+def test_sparse_attention_rejects_arguments(fn, call, kw, code):
+    assert call(fn, **kw) == code
+    assert last()
+
+
+def test_sparse_attention_null_shape_and_empty(fn):
+    assert fn["svdq_select_blocks"](P(A), P(A), None, None, P(A), P(A), 1 << 40, None) == INVALID
+    for kw in (dict(batch=0), dict(seq_q=0)):
+        s = _shape(**kw)
+        assert _select(fn, s, q=0, k=0, blocks=0, ws=0, ws_bytes=0) == OK
+        assert _block(fn, s, q=0, k=0, v=0, blocks=0, out=0, ws=0, ws_bytes=0) == OK
+        assert _sparse(fn, s, q=0, k=0, v=0, out=0, ws=0, ws_bytes=0) == OK
+        assert bdt.svdq_sparse_attention_workspace_bytes(s) == 0
+
+
+def test_sparse_attention_workspace_sizes():
+    # 64-bit means of 2 x 4 x 2 query and 2 x 2 x 5 key blocks of 128 columns
+    means = 2 * 4 * 2 * 128 * 8 + 2 * 2 * 5 * 128 * 8
+    assert bdt.svdq_select_blocks_workspace_bytes(_shape()) == means
+    assert bdt.svdq_sparse_attention_workspace_bytes(_shape()) >= means + 2 * 4 * 2 * 3 * 4
+    assert bdt.svdq_block_attention_workspace_bytes(_shape(batch=64, seq_q=4096)) == 0
+
+
+def test_attention_tensor_functions_refuse_bad_tensors():
+    bf = torch.bfloat16
+    q, k = torch.zeros(2, 4, 200, 64, dtype=bf), torch.zeros(2, 2, 300, 64, dtype=bf)
+    blocks = torch.zeros(2, 4, 2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        bdt.sparse_attention(q, k, k, 3)
+    with pytest.raises(ValueError, match="GPU"):
+        bdt.select_blocks(q, k, 3)
+    with pytest.raises(ValueError, match="GPU"):
+        bdt.block_attention(q, k, k, blocks)
+    with pytest.raises(ValueError, match="shape"):
+        bdt.block_attention(q, k, k, blocks[:, :, :1].contiguous())
+    with pytest.raises(ValueError, match="shape"):
+        bdt.sparse_attention(q, k, k[:, :, :299].contiguous(), 3)
+    with pytest.raises(ValueError, match="shape"):
+        bdt.sparse_attention(q, k[..., :32].contiguous(), k, 3)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.sparse_attention(q.transpose(1, 2).contiguous().transpose(1, 2), k, k, 3)
+    with pytest.raises(TypeError):
+        bdt.sparse_attention(q.float(), k, k, 3)
+    with pytest.raises(TypeError):
+        bdt.sparse_attention(q, k, k, 3, kv_len=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="shape"):
+        bdt.sparse_attention(q, k, k, 3, kv_len=torch.zeros(3, dtype=torch.int32))
