@@ -69,8 +69,9 @@ int32_t read_shape(const svdq_attention_shape *e, AttnShape &a) {
     a.planes_q = a.B * a.H;
     a.planes_k = a.B * a.G;
     SVDQ_TRY(check_rows(a.planes_q, "batch * heads"));
-    // the means (one workgroup per block), the choice, the attention, the join
-    SVDQ_TRY(check_grid(a.planes_q * a.nq + a.planes_k * a.nk, 256, "the block selection"));
+    // the means (one workgroup per block), the choice (fewer than one of 512 per
+    // query block), the attention, the join
+    SVDQ_TRY(check_grid(a.planes_q * a.nq + a.planes_k * a.nk, 512, "the block selection"));
     SVDQ_TRY(check_grid(a.planes_q * a.nq * attention_splits(a), 256, "the block attention"));
     return SVDQ_OK;
 }

@@ -21,9 +21,7 @@ __device__ __forceinline__ int64_t valid_keys(const int32_t *kv_len, int64_t b, 
 // Means over blocks of rows.  One workgroup per block of one head: 16-byte
 // loads, 16 (D = 128) or 32 (D = 64) rows at a time, 64-bit sums of eight
 // columns a thread, then a sum over the rows through LDS.  Bound by reading Q
-// and K once.  Query means are stored [block][D]; key means transposed,
-// [D][block], so that the score kernel's lanes (one key block each) read them
-// in runs.
+// and K once.
 template <int D>
 __global__ void __launch_bounds__(256)
 block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
@@ -63,11 +61,7 @@ block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ 
     }
     if (r0 == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double m = s[i] / rows;
-            if (query) qm[id * D + 8 * c + i] = m;
-            else km[(plane * D + 8 * c + i) * nb + blk] = m;
-        }
+        for (int i = 0; i < 8; ++i) (query ? qm : km)[id * D + 8 * c + i] = s[i] / rows;
     }
 }
 
@@ -81,96 +75,150 @@ __device__ __forceinline__ uint64_t order_key(double x) {
     return o ? o : 1;
 }
 
-// One workgroup per `R` query blocks of a head.  Scores: a thread takes key
-// block j for R query blocks (or, with `spread`, each wave R / 4 of them: few
-// key blocks leave threads idle otherwise), the query means uniform operands.
-// The keys go to LDS.  Choice: one wave per query block finds the largest
-// threshold that at least `keep` keys reach, bit by bit from the top (64
-// ballots at most; it ends early when exactly `keep` keys reach it), and
-// writes the numbers of the keys above it in ascending order, equal ones from
-// the lowest number up to the count.
-template <int D, int R, bool SPREAD>
-__global__ void __launch_bounds__(256)
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kChooseWaves = 8;
+
+// How many of a lane's NL keys (in registers; NL == 0: n keys in LDS) reach t,
+// summed over the wave.
+template <int NL>
+__device__ __forceinline__ int count_from(const uint64_t (&x)[NL ? NL : 1], const uint64_t *kr,
+                                          int nk, int lane, uint64_t t) {
+    int n = 0;
+    if (NL) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) n += __popcll(__ballot(x[i] >= t));
+    } else {
+        for (int j = lane; j < nk + lane; j += 64)          // all lanes take part
+            n += __popcll(__ballot(j < nk && kr[j < nk ? j : 0] >= t));
+    }
+    return n;
+}
+
+// The `keep` highest of a query block's keys, by one wave: the largest
+// threshold that at least `keep` keys reach, bit by bit below the first bit in
+// which the highest and the lowest key differ (one ballot per 64 keys and bit;
+// it ends early when exactly `keep` reach it), then the numbers of the keys
+// above it in ascending order, equal ones from the lowest number up to the
+// count.
+template <int NL>
+__device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, int keep, int lane,
+                                       int32_t *out) {
+    uint64_t x[NL ? NL : 1];
+    if (NL)
+#pragma unroll
+        for (int i = 0; i < NL; ++i) x[i] = 64 * i + lane < nk ? kr[64 * i + lane] : 0;
+    uint64_t at = 1;                                         // keys >= at are taken,
+    int ties = 0x7FFFFFFF;                                   // `ties` of those equal to it at most
+    if (valid > keep) {
+        uint64_t any = 0, all = ~0ull;                       // bits set in some / in every valid key
+        for (int j = lane; j < valid; j += 64) {
+            any |= kr[j];
+            all &= kr[j];
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            any |= __shfl_xor(any, d);
+            all &= __shfl_xor(all, d);
+        }
+        const uint64_t differ = any & ~all;
+        const int top = differ ? 63 - __builtin_clzll(differ) : -1;
+        at = top == 63 ? 0 : all & ~((2ull << (top < 0 ? 0 : top)) - 1);
+        if (top < 0) at = all;                               // all equal
+        bool exact = false;
+        for (int bit = top; bit >= 0 && !exact; --bit) {
+            const uint64_t t = at | 1ull << bit;
+            const int n = count_from<NL>(x, kr, nk, lane, t);
+            if (n >= keep) at = t;
+            exact = n == keep;
+        }
+        if (!exact) ties = at == ~0ull ? keep : keep - count_from<NL>(x, kr, nk, lane, at + 1);
+    }
+    int n = 0;
+    const uint64_t below = (1ull << lane) - 1;
+    for (int j = lane; j < nk + lane; j += 64) {
+        const uint64_t y = j < nk ? kr[j] : 0;
+        const uint64_t equal = __ballot(y == at);
+        const bool take = y > at || (y == at && __popcll(equal & below) < ties);
+        const uint64_t taken = __ballot(take);
+        const int pos = n + __popcll(taken & below);
+        if (take && pos < keep) out[pos] = j;
+        n += __popcll(taken);
+        ties -= __popcll(equal) < ties ? __popcll(equal) : ties;
+    }
+    for (int p = n + lane; p < keep; p += 64) out[p] = -1;
+}
+
+// One workgroup of eight waves per R <= 16 query blocks of a head.  Scores: 16
+// query blocks x 16 key blocks a tile on the 64-bit matrix instruction
+// (v_mfma_f64_16x16x4_f64: lane l supplies row / column l % 16, k = l / 16;
+// result element i is row 4 i + l / 16, column l % 16), the query means in
+// registers throughout, tiles of key blocks shared among the waves; the order
+// of k is free, so a lane takes two neighbouring columns in one 16-byte load.
+// The keys go to LDS, where a wave then chooses for each of its query blocks.
+template <int D>
+__global__ void __launch_bounds__(64 * kChooseWaves)
 block_choose_kernel(const double *__restrict__ qm, const double *__restrict__ km,
-                    const int32_t *__restrict__ kv_len, AttnShape a, int32_t *__restrict__ blocks) {
+                    const int32_t *__restrict__ kv_len, AttnShape a, int R,
+                    int32_t *__restrict__ blocks) {
     extern __shared__ uint64_t keys[];                       // [R][nk]
-    constexpr int RT = SPREAD ? R / 4 : R;                   // query blocks per thread
+    constexpr int STEPS = D / 8;                             // pairs of 16x16x4 products
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t per = (a.nq + R - 1) / R;
     const int64_t plane = blockIdx.x / per;
     const int64_t i0 = (blockIdx.x - plane * per) * R;
     const int64_t b = plane / a.H, h = plane - b * a.H;
     const int64_t kplane = b * a.G + h / (a.H / a.G);
-    const int64_t len = valid_keys(kv_len, b, a.seq_k);
-    const int nk = (int)a.nk, valid = (int)((len + kKB - 1) / kKB);
-    const int rt0 = SPREAD ? wave * RT : 0;
-    const double *kp = km + kplane * D * nk;
-    const double *qp[RT];
+    const int nk = (int)a.nk;
+    const int valid = (int)((valid_keys(kv_len, b, a.seq_k) + kKB - 1) / kKB);
+    const int c = lane & 15, g = lane >> 4;
+    f64x2 qf[STEPS];
+    {
+        int64_t i = i0 + (c < R ? c : R - 1);
+        if (i >= a.nq) i = a.nq - 1;
+        const double *p = qm + (plane * a.nq + i) * D + 2 * g;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int64_t i = i0 + rt0 + r;
-        qp[r] = qm + (plane * a.nq + (i < a.nq ? i : a.nq - 1)) * D;
+        for (int s = 0; s < STEPS; ++s) qf[s] = *reinterpret_cast<const f64x2 *>(p + 8 * s);
     }
-    for (int j = SPREAD ? lane : (int)threadIdx.x; j < nk; j += SPREAD ? 64 : 256) {
-        double s[RT] = {};
-        if (j < valid && j >= a.first) {
-#pragma unroll 8
-            for (int d = 0; d < D; ++d) {
-                const double x = kp[(int64_t)d * nk + j];
+    for (int j0 = 16 * wave; j0 < nk; j0 += 16 * kChooseWaves) {
+        const int j = j0 + c;
+        f64x4 acc = {};
+        if (j0 < valid) {                                    // uniform
+            // blocks without a valid key have no mean: read another, never used
+            const double *p = km + (kplane * nk + (j < valid ? j : valid - 1)) * D + 2 * g;
+            f64x2 kf[STEPS];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) s[r] = fma(qp[r][d], x, s[r]);
+            for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f64x2 *>(p + 8 * s);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].x, kf[s].x, acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].y, kf[s].y, acc, 0, 0, 0);
             }
         }
+        if (j < nk)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            keys[(rt0 + r) * nk + j] = j >= valid ? 0ull : j < a.first ? ~0ull : order_key(s[r]);
+            for (int i = 0; i < 4; ++i)
+                if (4 * i + g < R)
+                    keys[(4 * i + g) * nk + j] =
+                        j >= valid ? 0ull : j < a.first ? ~0ull : order_key(acc[i]);
     }
     __syncthreads();
-    for (int r = wave; r < R; r += 4) {
-        const int64_t i = i0 + r;
-        if (i >= a.nq) break;
+    for (int r = wave; r < R; r += kChooseWaves) {
+        if (i0 + r >= a.nq) break;
         const uint64_t *kr = keys + r * nk;
-        int32_t *out = blocks + (plane * a.nq + i) * a.keep;
-        uint64_t at = 1;                                     // threshold: keys >= at are taken,
-        int ties = 0x7FFFFFFF;                               // of those equal to it `ties` at most
-        if (valid > a.keep) {
-            at = 0;
-            bool exact = false;
-            for (int bit = 63; bit >= 0 && !exact; --bit) {
-                const uint64_t t = at | 1ull << bit;
-                int n = 0;
-                for (int j = lane; j < nk + lane; j += 64)   // all lanes take part
-                    n += __popcll(__ballot(j < nk && kr[j < nk ? j : 0] >= t));
-                if (n >= a.keep) at = t;
-                exact = n == a.keep;
-            }
-            if (!exact) {
-                int above = 0;
-                for (int j = lane; j < nk + lane; j += 64)
-                    above += __popcll(__ballot(j < nk && kr[j < nk ? j : 0] > at));
-                ties = a.keep - above;
-            }
-        }
-        int n = 0;
-        for (int j = lane; j < nk + lane; j += 64) {
-            const uint64_t x = j < nk ? kr[j] : 0;
-            const uint64_t below = (1ull << lane) - 1;
-            const uint64_t equal = __ballot(x == at);
-            const bool take = x > at || (x == at && __popcll(equal & below) < ties);
-            const uint64_t taken = __ballot(take);
-            const int pos = n + __popcll(taken & below);
-            if (take && pos < a.keep) out[pos] = j;
-            n += __popcll(taken);
-            ties -= __popcll(equal) < ties ? __popcll(equal) : ties;
-        }
-        for (int p = n + lane; p < a.keep; p += 64) out[p] = -1;
+        int32_t *out = blocks + (plane * a.nq + i0 + r) * a.keep;
+        if (nk <= 128) choose<2>(kr, nk, valid, a.keep, lane, out);
+        else if (nk <= 512) choose<8>(kr, nk, valid, a.keep, lane, out);
+        else choose<0>(kr, nk, valid, a.keep, lane, out);
     }
 }
 
 namespace {
 
-// Query blocks per workgroup: their keys fit 32 KB of LDS.
-int choose_rows(int64_t nk) { return nk <= 512 ? 8 : nk <= 1024 ? 4 : nk <= 2048 ? 2 : 1; }
+// Query blocks per workgroup: their keys fit 64 KB of LDS (two workgroups per
+// compute unit), or 128 KB for the longest sequences.
+int choose_rows(int64_t nk) { return nk <= 512 ? 16 : nk <= 1024 ? 8 : 4; }
 
 template <int D>
 hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, const AttnShape &a,
@@ -182,19 +230,10 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, c
         q, k, kv_len, a, qm, km);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int R = choose_rows(a.nk);
+    const int R = (int)(choose_rows(a.nk) < a.nq ? choose_rows(a.nk) : a.nq);
     const unsigned grid = (unsigned)(a.planes_q * ((a.nq + R - 1) / R));
-    const size_t lds = (size_t)R * a.nk * 8;
-    if (R == 8 && a.nk <= 128)
-        block_choose_kernel<D, 8, true><<<grid, 256, lds, stream>>>(qm, km, kv_len, a, blocks);
-    else if (R == 8)
-        block_choose_kernel<D, 8, false><<<grid, 256, lds, stream>>>(qm, km, kv_len, a, blocks);
-    else if (R == 4)
-        block_choose_kernel<D, 4, false><<<grid, 256, lds, stream>>>(qm, km, kv_len, a, blocks);
-    else if (R == 2)
-        block_choose_kernel<D, 2, false><<<grid, 256, lds, stream>>>(qm, km, kv_len, a, blocks);
-    else
-        block_choose_kernel<D, 1, false><<<grid, 256, lds, stream>>>(qm, km, kv_len, a, blocks);
+    block_choose_kernel<D><<<grid, 64 * kChooseWaves, (size_t)R * a.nk * 8, stream>>>(
+        qm, km, kv_len, a, R, blocks);
     return hipGetLastError();
 }
 

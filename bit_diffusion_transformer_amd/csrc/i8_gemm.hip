@@ -60,15 +60,17 @@ struct Tile {
     static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
     static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks per wave
     static constexpr int STAGE = (BM + BN) * kRow;
-    static constexpr int LOADS = (BM + BN) / 8 / WAVES;          // per wave and stage
+    static constexpr int CW = BN / 8 / WAVES;                    // copies per wave and stage, W
+    static constexpr int LOADS = CW + BM / 8 / WAVES;            // and both operands
     static constexpr int SEGS = NB * 4;               // 16-byte segments of a staged output row
     static constexpr int OUT = MB * 32 * SEGS * 16;   // a wave's staged output
     static constexpr int LDS = NBUF * STAGE > WAVES * OUT ? NBUF * STAGE : WAVES * OUT;
-    static_assert(BM == BN && BM % (4 * WAVES) == 0, "half of the waves copy each operand");
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole copies per wave");
+    static_assert((SEGS & (SEGS - 1)) == 0, "the staging swizzle");
 };
 
 template <class T>
-__global__ void __launch_bounds__(T::THREADS)
+__global__ void __launch_bounds__(T::THREADS, T::WAVES == 8 ? 2 : 1)
 i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
                const int8_t *__restrict__ qw, const float *__restrict__ sw,
                const uint16_t *__restrict__ bias, int act, int64_t M, int64_t N, int64_t K,
@@ -87,38 +89,35 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
     }
 
     // Copies of a stage: 1 KB each, 8 rows; lane l carries row l / 8 into slot
-    // l % 8.  Rows past the matrix re-read its last row (never stored).  The
+    // l % 8.  Copy i of wave w: weight rows 8 (w + WAVES i) for i < CW, then token
+    // rows.  Rows past the matrix re-read its last row (never stored).  The
     // second half of a stage that holds only 64 bytes re-reads the first (its
     // products are left out).
-    // Waves 0 .. WAVES/2 - 1 carry weight rows (BM == BN), the others token rows.
-    const bool carry_w = wave < T::WAVES / 2;
-    const int8_t *src = carry_w ? qw + n0 * K : qa + m0 * K;
     uint32_t off[T::LOADS];
-    const int row0 = (wave % (T::WAVES / 2)) * T::LOADS * 8 + lane / 8;
-    {
-        const int64_t left = carry_w ? N - n0 : M - m0;
+    const int row0 = 8 * wave + lane / 8;            // of copy 0; later ones 8 WAVES further
 #pragma unroll
-        for (int i = 0; i < T::LOADS; ++i) {
-            const int row = row0 + 8 * i;
-            const uint32_t r = row < left ? row : (uint32_t)left - 1;
-            off[i] = r * (uint32_t)K + 16 * ((lane & 7) ^ swz(row));
-        }
+    for (int i = 0; i < T::LOADS; ++i) {
+        const int row = row0 + 8 * T::WAVES * (i < T::CW ? i : i - T::CW);
+        const int64_t left = i < T::CW ? N - n0 : M - m0;
+        const uint32_t r = row < left ? row : (uint32_t)left - 1;
+        off[i] = r * (uint32_t)K + 16 * ((lane & 7) ^ swz(row));
     }
+    const int8_t *w0 = qw + n0 * K, *x0 = qa + m0 * K;
     const int nf = (int)(K / kRow);                  // whole stages
     const bool half = (K & 64) != 0;                 // then one of 64 bytes
     const int ns = nf + (half ? 1 : 0);
     auto issue = [&](int s) {
-        uint8_t *st = lds + (s % T::NBUF) * T::STAGE + wave * T::LOADS * 1024;
-        const int8_t *g = src + (int64_t)s * kRow;
+        uint8_t *st = lds + (s % T::NBUF) * T::STAGE + wave * 1024;
+        const int64_t g = (int64_t)s * kRow;
         const bool last = s == nf;
 #pragma unroll
         for (int i = 0; i < T::LOADS; ++i) {
             uint32_t o = off[i];
             if (last) {                              // segment seg -> seg % 4
-                const int seg = (lane & 7) ^ swz(row0 + 8 * i);
-                o -= 16 * (seg & 4);
+                const int row = row0 + 8 * T::WAVES * (i < T::CW ? i : i - T::CW);
+                o -= 16 * (((lane & 7) ^ swz(row)) & 4);
             }
-            copy16_to_lds(g + o, st + i * 1024);
+            copy16_to_lds((i < T::CW ? w0 : x0) + g + o, st + i * T::WAVES * 1024);
         }
     };
 
@@ -221,7 +220,10 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
     }
 }
 
-typedef Tile<256, 256, 4, 2, 2> Big;
+// Tall tiles: 256 channels x 64 MB tokens, eight waves 2 (tokens) x 4
+// (channels), 32 MB x 64 each; one workgroup per compute unit.
+template <int BM>
+using Tall = Tile<BM, 256, 2, 4, 2>;
 typedef Tile<128, 128, 2, 2, 2> Mid;
 typedef Tile<64, 64, 2, 2, 4> Small;
 
@@ -242,16 +244,29 @@ hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, c
                           uint16_t *Y, void *workspace, hipStream_t stream) {
     (void)workspace;
     const int64_t cus = wg_slots() / 2;
-    if (tiles<Big>(M, N) >= cus)
-        i8_gemm_kernel<Big><<<(unsigned)tiles<Big>(M, N), Big::THREADS, 0, stream>>>(
+    auto run = [&](auto t) {
+        typedef decltype(t) T;
+        i8_gemm_kernel<T><<<(unsigned)tiles<T>(M, N), T::THREADS, 0, stream>>>(
             qa, sa, qw, sw, bias, act, M, N, K, Y);
-    else if (tiles<Mid>(M, N) >= cus)
-        i8_gemm_kernel<Mid><<<(unsigned)tiles<Mid>(M, N), Mid::THREADS, 0, stream>>>(
-            qa, sa, qw, sw, bias, act, M, N, K, Y);
-    else
-        i8_gemm_kernel<Small><<<(unsigned)tiles<Small>(M, N), Small::THREADS, 0, stream>>>(
-            qa, sa, qw, sw, bias, act, M, N, K, Y);
-    return hipGetLastError();
+        return hipGetLastError();
+    };
+    if (tiles<Tall<256>>(M, N) >= cus) {
+        // The height with the shortest time for the whole rounds of compute
+        // units that its tiles take, a tile's time taken as its height + 16.
+        int best = 0;
+        int64_t least = 0;
+        for (int bm = 128; bm <= 320; bm += 64) {
+            const int64_t n = (M + bm - 1) / bm * ((N + 255) / 256);
+            const int64_t cost = (n + cus - 1) / cus * (bm + 16);
+            if (!best || cost < least) best = bm, least = cost;
+        }
+        if (best == 128) return run(Tall<128>());
+        if (best == 192) return run(Tall<192>());
+        if (best == 256) return run(Tall<256>());
+        return run(Tall<320>());
+    }
+    if (tiles<Mid>(M, N) >= cus) return run(Mid());
+    return run(Small());
 }
 
 }  // namespace svdq

@@ -7,32 +7,44 @@ namespace svdq {
 
 namespace {
 
-constexpr int kThreads = 256;
-
-// Eight consecutive values of a row, as fp32.
+// Eight consecutive values of a row as they are loaded (16 bytes of bf16, 32 of
+// fp32), and as fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void *X, int64_t at, float (&v)[8]) {
-    if (F32) {
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(static_cast<const float *>(X) + at);
-        const f32x4 a = p[0], b = p[1];
+struct Raw {
+    u32x4 w[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_raw(const void *X, int64_t at) {
+    Raw<F32> r;
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const char *>(X) + at * (F32 ? 4 : 2));
+    r.w[0] = p[0];
+    if (F32) r.w[F32 ? 1 : 0] = p[1];
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void values(const Raw<F32> &r, float (&v)[8]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = a[j];
-            v[4 + j] = b[j];
-        }
-    } else {
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(X) + at);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = bf16_lo(x[j]);
-            v[2 * j + 1] = bf16_hi(x[j]);
+    for (int j = 0; j < 4; ++j) {
+        if (F32) {
+            v[j] = __uint_as_float(r.w[0][j]);
+            v[4 + j] = __uint_as_float(r.w[F32 ? 1 : 0][j]);
+        } else {
+            v[2 * j] = bf16_lo(r.w[0][j]);
+            v[2 * j + 1] = bf16_hi(r.w[0][j]);
         }
     }
 }
 
 __device__ __forceinline__ void load_inv(const float *lam, int k, float (&inv)[8]) {
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(lam + k);
+    const f32x4 x = p[0], y = p[1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) inv[j] = lam ? 1.0f / lam[k + j] : 1.0f;
+    for (int j = 0; j < 4; ++j) {
+        inv[j] = 1.0f / x[j];
+        inv[4 + j] = 1.0f / y[j];
+    }
 }
 
 // rint(fl32(v inv)) as the low byte of v inv + 1.5 * 2^23 (the addition rounds
@@ -60,11 +72,14 @@ __device__ __forceinline__ float wave_max(float x) {
 
 // The largest of `x` over the workgroup; `slot` alternates between calls, so
 // that one barrier a call is enough.
-__device__ __forceinline__ float group_max(float x, float (*part)[kThreads / 64], int slot) {
+template <int WAVES>
+__device__ __forceinline__ float group_max(float x, float (*part)[WAVES], int slot) {
     x = wave_max(x);
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = x;
     __syncthreads();
-    return fmaxf(fmaxf(part[slot][0], part[slot][1]), fmaxf(part[slot][2], part[slot][3]));
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) x = fmaxf(x, part[slot][w]);
+    return x;
 }
 
 __device__ __forceinline__ float scale_of(float amax, float &inv) {
@@ -78,78 +93,87 @@ __device__ __forceinline__ float scale_of(float amax, float &inv) {
 }
 
 // One workgroup per `rows` consecutive rows; thread t holds the pieces of 8
-// values at 8 (t + 256 c), c < CH, of the row at hand in registers, so each
+// values at 8 (t + THREADS c), c < CH, of the row at hand in registers, so each
 // row is read once, and the reciprocals of its smoothing factors across the
 // rows (a correctly rounded division costs about as much as everything else
 // here together).  The next row is loaded before the current one is reduced.
 // Bound by memory: 2 bytes read and 1 written per element (4 and 1 for W).
-template <int CH, bool F32>
-__global__ void __launch_bounds__(kThreads)
+template <int THREADS, int CH, bool F32, bool SMOOTH>
+__global__ void __launch_bounds__(THREADS)
 i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ lam, int64_t M, int64_t K,
                    int rows, int8_t *__restrict__ q, float *__restrict__ s) {
-    __shared__ float part[2][kThreads / 64];
+    __shared__ float part[2][THREADS / 64];
     const int64_t m0 = (int64_t)blockIdx.x * rows;
     const int64_t m1 = m0 + rows < M ? m0 + rows : M;
-    float inv[CH][8], next[CH][8];
+    Raw<F32> next[CH];
+    float inv[SMOOTH ? CH : 1][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int k = 8 * ((int)threadIdx.x + kThreads * c);
-        if (k < K) {
-            load8<F32>(X, m0 * K + k, next[c]);
-            if (!F32) load_inv(lam, k, inv[c]);
-        }
+        const int k = 8 * ((int)threadIdx.x + THREADS * c);
+        if (k < K) next[c] = load_raw<F32>(X, m0 * K + k);
     }
+    if (SMOOTH)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = 8 * ((int)threadIdx.x + THREADS * c);
+            if (k < K) load_inv(lam, k, inv[SMOOTH ? c : 0]);
+        }
     for (int64_t m = m0; m < m1; ++m) {
         float v[CH][8], amax = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = 8 * ((int)threadIdx.x + kThreads * c);
+            const int k = 8 * ((int)threadIdx.x + THREADS * c);
             if (k < K) {
+                values<F32>(next[c], v[c]);
+                if (m + 1 < m1) next[c] = load_raw<F32>(X, (m + 1) * K + k);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[c][j] = F32 ? next[c][j] : next[c][j] * inv[c][j];
+                    if (SMOOTH) v[c][j] *= inv[SMOOTH ? c : 0][j];
                     amax = fmaxf(amax, fabsf(v[c][j]));
                 }
-                if (m + 1 < m1) load8<F32>(X, (m + 1) * K + k, next[c]);
             }
         }
-        amax = group_max(amax, part, (int)(m - m0) & 1);
+        amax = group_max<THREADS / 64>(amax, part, (int)(m - m0) & 1);
         float r;
         const float scale = scale_of(amax, r);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = 8 * ((int)threadIdx.x + kThreads * c);
+            const int k = 8 * ((int)threadIdx.x + THREADS * c);
             if (k < K) *reinterpret_cast<u32x2 *>(q + m * K + k) = codes8(v[c], r);
         }
         if (threadIdx.x == 0) s[m] = scale;
     }
 }
 
-// Rows too long for the registers: the row is read twice (the second time
-// mostly from the caches).
+// Rows too long for the registers (K > 16384): the row is read twice (the
+// second time mostly from the caches).
+constexpr int kLong = 512;
+
 template <bool F32>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kLong)
 i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ lam, int64_t K,
                         int8_t *__restrict__ q, float *__restrict__ s) {
-    __shared__ float part[1][kThreads / 64];
+    __shared__ float part[1][kLong / 64];
     const int64_t m = blockIdx.x;
     float amax = 0.0f, v[8], inv[8];
-    for (int k = 8 * (int)threadIdx.x; k < K; k += 8 * kThreads) {
-        load8<F32>(X, m * K + k, v);
-        if (!F32) load_inv(lam, k, inv);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(F32 ? v[j] : v[j] * inv[j]));
-    }
-    amax = group_max(amax, part, 0);
-    float r;
-    const float scale = scale_of(amax, r);
-    for (int k = 8 * (int)threadIdx.x; k < K; k += 8 * kThreads) {
-        load8<F32>(X, m * K + k, v);
-        if (!F32) {
+    auto load = [&](int k) {
+        values<F32>(load_raw<F32>(X, m * K + k), v);
+        if (lam) {
             load_inv(lam, k, inv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= inv[j];
         }
+    };
+    for (int k = 8 * (int)threadIdx.x; k < K; k += 8 * kLong) {
+        load(k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    }
+    amax = group_max<kLong / 64>(amax, part, 0);
+    float r;
+    const float scale = scale_of(amax, r);
+    for (int k = 8 * (int)threadIdx.x; k < K; k += 8 * kLong) {
+        load(k);
         *reinterpret_cast<u32x2 *>(q + m * K + k) = codes8(v, r);
     }
     if (threadIdx.x == 0) s[m] = scale;
@@ -159,30 +183,34 @@ i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ la
 // rows once there are workgroups enough to fill the chip without.
 int rows_per_group(int64_t M) { return M >= 4096 ? 4 : M >= 2048 ? 2 : 1; }
 
+template <int THREADS, int CH, bool F32>
+void start(const void *X, const float *lam, int64_t M, int64_t K, int8_t *q, float *s,
+           hipStream_t stream) {
+    const int rows = rows_per_group(M);
+    const unsigned grid = (unsigned)((M + rows - 1) / rows);
+    if (!F32 && lam)
+        i8_quantize_kernel<THREADS, CH, F32, !F32><<<grid, THREADS, 0, stream>>>(X, lam, M, K, rows, q, s);
+    else
+        i8_quantize_kernel<THREADS, CH, F32, false><<<grid, THREADS, 0, stream>>>(X, lam, M, K, rows, q, s);
+}
+
+// 256 threads up to K = 4096, then 512 (three pieces at K = 12288: the
+// registers of a thread leave room for two workgroups per SIMD's waves).
 template <bool F32>
 hipError_t launch(const void *X, const float *lam, int64_t M, int64_t K, int8_t *q, float *s,
                   hipStream_t stream) {
-    const int pieces = (int)((K / 8 + kThreads - 1) / kThreads);
-    if (pieces > 8) {
-        i8_quantize_long_kernel<F32><<<(unsigned)M, kThreads, 0, stream>>>(X, lam, K, q, s);
-        return hipGetLastError();
-    }
-    const int rows = rows_per_group(M);
-    const unsigned grid = (unsigned)((M + rows - 1) / rows);
-    if (pieces == 1)
-        i8_quantize_kernel<1, F32><<<grid, kThreads, 0, stream>>>(X, lam, M, K, rows, q, s);
-    else if (pieces == 2)
-        i8_quantize_kernel<2, F32><<<grid, kThreads, 0, stream>>>(X, lam, M, K, rows, q, s);
-    else if (pieces <= 4)
-        i8_quantize_kernel<4, F32><<<grid, kThreads, 0, stream>>>(X, lam, M, K, rows, q, s);
-    else
-        i8_quantize_kernel<8, F32><<<grid, kThreads, 0, stream>>>(X, lam, M, K, rows, q, s);
+    if (K <= 2048) start<256, 1, F32>(X, lam, M, K, q, s, stream);
+    else if (K <= 4096) start<256, 2, F32>(X, lam, M, K, q, s, stream);
+    else if (K <= 8192) start<512, 2, F32>(X, lam, M, K, q, s, stream);
+    else if (K <= 12288) start<512, 3, F32>(X, lam, M, K, q, s, stream);
+    else if (K <= 16384) start<512, 4, F32>(X, lam, M, K, q, s, stream);
+    else i8_quantize_long_kernel<F32><<<(unsigned)M, kLong, 0, stream>>>(X, lam, K, q, s);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t i8_quantize_groups(int64_t M, int64_t K) { return M; }
+int64_t i8_quantize_groups(int64_t M) { return M; }
 
 hipError_t launch_i8_quantize(const void *X, bool fp32, const float *lambda, int64_t M, int64_t K,
                               int8_t *q, float *s, hipStream_t stream) {
