@@ -15,6 +15,8 @@
 #include "attention_internal.h"
 #include "svdq_device.h"
 
+#include <type_traits>
+
 namespace svdq {
 
 namespace attn {
@@ -29,6 +31,12 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 // Every vector-memory instruction of this wave done and its LDS reads returned.
 __device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x7 << 4); }
 
+// c plus the two bf16 values of x (products with one): the sum of the weights as
+// they enter the second product, rounded, in half the instructions.
+__device__ __forceinline__ float add_pair(uint32_t x, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x),
+                                           __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
+}
 __device__ __forceinline__ float max_both_halves(float x) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
@@ -40,15 +48,15 @@ __device__ __forceinline__ float sum_both_halves(float x) {
 
 // LDS layout of a K or V block: rows of D values, 16-byte segments XORed by a
 // function of the row.  K: eight (sixteen) consecutive rows of one segment hit
-// different banks.  V: four consecutive rows of two neighbouring segments do
-// (what a 16-lane group of the transposing read touches).
+// different banks.  V: four consecutive rows of four neighbouring segments do
+// (what 32 lanes of the transposing read touch).
 template <int D>
 __device__ __forceinline__ int swz_k(int row) {
     return D == 128 ? row & 15 : (row & 7) ^ ((row >> 3) & 1);
 }
 template <int D>
 __device__ __forceinline__ int swz_v(int row) {
-    return D == 128 ? 2 * (row & 7) : 2 * (row & 3);
+    return D == 128 ? 4 * (row & 3) : 2 * (row & 3);
 }
 
 // Transposing LDS read: within each 16 lanes, lane i supplies 8 bytes (4 columns)
@@ -107,14 +115,8 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5, col = lane & 31;
 
-    // Consecutive workgroups go to the 8 XCDs in turn: each gets a contiguous
-    // range of the query blocks, whose lists share key blocks in its L2.
-    int64_t id;
-    {
-        const int64_t n = a.planes_q * a.nq * (SPLIT ? splits : 1);
-        const int64_t x = blockIdx.x & 7, per = n >> 3, r = n & 7;
-        id = x * per + (x < r ? x : r) + (blockIdx.x >> 3);
-    }
+    // contiguous query blocks per XCD: their lists share key blocks in its L2
+    int64_t id = xcd_range(blockIdx.x, a.planes_q * a.nq * (SPLIT ? splits : 1));
     const int piece = SPLIT ? (int)(id % splits) : 0;
     if (SPLIT) id /= splits;
     const int64_t plane = id / a.nq, qi = id - plane * a.nq;
@@ -139,19 +141,36 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
     const uint8_t *vb = reinterpret_cast<const uint8_t *>(v + kplane * a.seq_k * D);
     // Rows at or past the sequence's length re-read its last valid row: their
     // scores are masked, and their weights are zeros times finite values.
-    auto issue = [&](int i) {
-        const int buf = (i - first) & 1, n0 = (int)lds.list[i] * kKB;
+    const int cp_row = wave * COPIES * RPT + lane / SEGS, cp_slot = lane % SEGS;
+    uint32_t k_at[COPIES], v_at[COPIES];           // byte offsets within a block
 #pragma unroll
-        for (int c = 0; c < COPIES; ++c) {
-            const int row = (wave * COPIES + c) * RPT + lane / SEGS, slot = lane % SEGS;
-            const int n = n0 + row < len ? n0 + row : len - 1;
-            const uint32_t at = (uint32_t)n * (D * 2);
-            const int dst = (wave * COPIES + c) * 1024;
-            copy16_to_lds(kb + at + 16 * (slot ^ swz_k<D>(row)), lds.k[buf] + dst);
-            copy16_to_lds(vb + at + 16 * (slot ^ swz_v<D>(row)), lds.v[buf] + dst);
+    for (int c = 0; c < COPIES; ++c) {
+        const int row = cp_row + c * RPT;
+        k_at[c] = row * (D * 2) + 16 * (cp_slot ^ swz_k<D>(row));
+        v_at[c] = row * (D * 2) + 16 * (cp_slot ^ swz_v<D>(row));
+    }
+    auto issue = [&](int i, auto buffer) {
+        constexpr int BUF = decltype(buffer)::value;
+        const int n0 = __builtin_amdgcn_readfirstlane(lds.list[i]) * kKB, left = len - n0;
+        const uint8_t *k0 = kb + (int64_t)n0 * (D * 2), *v0 = vb + (int64_t)n0 * (D * 2);
+        uint8_t *kd = lds.k[BUF] + wave * COPIES * 1024, *vd = lds.v[BUF] + wave * COPIES * 1024;
+        if (__builtin_expect(left >= kKB, 1)) {
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c) {
+                copy16_to_lds(k0 + k_at[c], kd + c * 1024);
+                copy16_to_lds(v0 + v_at[c], vd + c * 1024);
+            }
+        } else {                                   // the block of the last key
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c) {
+                const int row = cp_row + c * RPT;
+                const uint32_t back = row < left ? 0 : (uint32_t)(row - left + 1) * (D * 2);
+                copy16_to_lds(k0 + (k_at[c] - back), kd + c * 1024);
+                copy16_to_lds(v0 + (v_at[c] - back), vd + c * 1024);
+            }
         }
     };
-    if (first < last) issue(first);
+    if (first < last) issue(first, std::integral_constant<int, 0>());
 
     // This lane's query, rows past the last re-reading it (never stored).
     const int64_t row0 = qi * kQB + wave * 32;
@@ -164,38 +183,70 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
         for (int s = 0; s < DK; ++s) qf[s] = *reinterpret_cast<const u32x4 *>(p + 16 * s);
     }
 
-    // LDS offsets: K row `col`, segment 2 s + h2 of step s; V: lane i of a
-    // 16-lane group supplies row i / 4 of four keys, 4 columns from 4 (i % 4) of
-    // the group's 16, and gets column i of the four rows.
-    int v_row, v_sub;
+    // LDS offsets (of buffer 0): K row `col` (and 32 further), segment 2 t + h2 of
+    // step t; V: lane i of a 16-lane group supplies row i / 4 of four keys, 4
+    // columns from 4 (i % 4) of the group's 16, and gets column i of the four
+    // rows; a step of 16 keys is 16 rows further (the same swizzle).
+    const uint8_t *k_rd[DK], *v_rd[DB];
+#pragma unroll
+    for (int t = 0; t < DK; ++t)
+        k_rd[t] = lds.k[0] + col * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(col));
     {
-        const int i = lane & 15;
-        v_row = 4 * h2 + (i >> 2);
-        v_sub = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);     // segment within a 32-wide block
+        const int i = lane & 15, row = 4 * h2 + (i >> 2);
+        const int sub = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);     // segment of a 32-wide block
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            v_rd[d] = lds.v[0] + row * (D * 2) + 16 * ((4 * d + sub) ^ swz_v<D>(row)) + 8 * (lane & 1);
     }
-    const int v_byte = 8 * (lane & 1);
 
     f32x16 o[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[d] = f32x16{};
     float m = -__builtin_inff(), l = 0.0f;
 
-    for (int i = first; i < last; ++i) {
-        const int buf = (i - first) & 1, n0 = (int)lds.list[i] * kKB;
+    auto block = [&](int i, auto buffer) {
+        constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
+        const int n0 = __builtin_amdgcn_readfirstlane(lds.list[i]) * kKB;
         wait_all();
         barrier();
-        if (i + 1 < last) issue(i + 1);
-        if (!active) continue;
+        if (i + 1 < last) issue(i + 1, std::integral_constant<int, 1 - BUF>());
+        if (!active) return;
         f32x16 s[2] = {f32x16{}, f32x16{}};
+        {
+            // fragments two steps ahead of the products that use them
+            u32x4 kf[3][2];
+            auto load = [&](int t) {
 #pragma unroll
-        for (int t = 0; t < DK; ++t)
+                for (int kk = 0; kk < 2; ++kk) {
+                    kf[t % 3][kk] = *reinterpret_cast<const u32x4 *>(k_rd[t] + AT + 32 * kk * (D * 2));
+                }
+            };
+            load(0);
+            load(1);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int row = 32 * kk + col;
-                const u32x4 kf = *reinterpret_cast<const u32x4 *>(
-                    lds.k[buf] + row * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(row)));
-                s[kk] = mfma_bf16_32x32x16(kf, qf[t], s[kk]);
+            for (int t = 0; t < DK; ++t) {
+                if (t + 2 < DK) load(t + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) s[kk] = mfma_bf16_32x32x16(kf[t % 3][kk], qf[t], s[kk]);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        }
+        // V fragments of a step of 16 keys (kk, t): keys 0 .. 3 and 8 .. 11 past
+        // 4 h2, every 32-wide block of columns
+        u32x4 vf[2][DB];
+        auto load_v = [&](int st) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const u32x2 y = read_transposed(v_rd[d] + AT + (16 * st + 8 * u) * (D * 2));
+                    vf[st & 1][d][2 * u] = y.x;
+                    vf[st & 1][d][2 * u + 1] = y.y;
+                }
+        };
+        load_v(0);
+        __builtin_amdgcn_sched_barrier(0);
         if (n0 + kKB > len) {                      // the sequence ends in this block
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
@@ -231,31 +282,25 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 s[kk][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kk][e], scale_log2, -off));
-                l += s[kk][e];
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
+                for (int w = 0; w < 4; ++w) {
                     p[kk][t][w] = pack_bf16x2(s[kk][8 * t + 2 * w], s[kk][8 * t + 2 * w + 1]);
+                    l = add_pair(p[kk][t][w], l);
+                }
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int st = 0; st < 4; ++st) {
+            if (st < 3) load_v(st + 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    u32x4 vf;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {  // keys 0 .. 3 and 8 .. 11 past 4 h2
-                        const int row = 32 * kk + 16 * t + 8 * u + v_row;
-                        const int at = row * (D * 2) + 16 * ((4 * d + v_sub) ^ swz_v<D>(row)) + v_byte;
-                        const u32x2 y = read_transposed(lds.v[buf] + at);
-                        vf[2 * u] = y.x;
-                        vf[2 * u + 1] = y.y;
-                    }
-                    o[d] = mfma_bf16_32x32x16(vf, p[kk][t], o[d]);
-                }
+            for (int d = 0; d < DB; ++d) o[d] = mfma_bf16_32x32x16(vf[st & 1][d], p[st >> 1][st & 1], o[d]);
+        }
+    };
+    for (int i = first; i < last; i += 2) {
+        block(i, std::integral_constant<int, 0>());
+        if (i + 1 < last) block(i + 1, std::integral_constant<int, 1>());
     }
     if (!active) return;
 

@@ -18,19 +18,33 @@ __device__ __forceinline__ int64_t valid_keys(const int32_t *kv_len, int64_t b, 
     return n < 0 ? 0 : n > seq_k ? seq_k : n;
 }
 
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+// Means of a head: tiles of 16 blocks; within one, column pair 2 p (p < D / 2)
+// of block c is the 16-byte element (p / 4) 64 + (p % 4) 16 + c.
+template <int D>
+__device__ __forceinline__ int64_t mean_at(int64_t blk, int p) {
+    return (blk >> 4) * (8 * D) + (p >> 2) * 64 + (p & 3) * 16 + (blk & 15);
+}
+__host__ __device__ inline int64_t mean_tiles(int64_t blocks) { return (blocks + 15) / 16; }
+
 // Means over blocks of rows.  One workgroup per block of one head: 16-byte
 // loads, 16 (D = 128) or 32 (D = 64) rows at a time, 64-bit sums of eight
 // columns a thread, then a sum over the rows through LDS.  Bound by reading Q
-// and K once.
+// and K once.  Stored in the order in which the score kernel's matrix
+// instruction takes them (mean_at), so that each of its loads is one run.
 template <int D>
 __global__ void __launch_bounds__(256)
 block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
-                   const int32_t *__restrict__ kv_len, AttnShape a, double *__restrict__ qm,
-                   double *__restrict__ km) {
+                   const int32_t *__restrict__ kv_len, AttnShape a, f64x2 *__restrict__ qm,
+                   f64x2 *__restrict__ km) {
     constexpr int LANES = D / 8, ROWS = 256 / LANES;
     __shared__ double part[ROWS / 2][D];
-    const bool query = blockIdx.x < a.planes_q * a.nq;       // uniform
-    const int64_t id = query ? blockIdx.x : blockIdx.x - a.planes_q * a.nq;
+    // neighbouring blocks' means share cache lines: one XCD writes them
+    const int64_t wg = xcd_range(blockIdx.x, a.planes_q * a.nq + a.planes_k * a.nk);
+    const bool query = wg < a.planes_q * a.nq;               // uniform
+    const int64_t id = query ? wg : wg - a.planes_q * a.nq;
     const int64_t nb = query ? a.nq : a.nk, size = query ? kQB : kKB;
     const int64_t plane = id / nb, blk = id - plane * nb;
     const int64_t seq = query ? a.seq_q : a.seq_k;
@@ -61,7 +75,9 @@ block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ 
     }
     if (r0 == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) (query ? qm : km)[id * D + 8 * c + i] = s[i] / rows;
+        for (int i = 0; i < 4; ++i)
+            (query ? qm : km)[plane * mean_tiles(nb) * (8 * D) + mean_at<D>(blk, 4 * c + i)] =
+                f64x2{s[2 * i] / rows, s[2 * i + 1] / rows};
     }
 }
 
@@ -75,33 +91,16 @@ __device__ __forceinline__ uint64_t order_key(double x) {
     return o ? o : 1;
 }
 
-typedef double f64x2 __attribute__((ext_vector_type(2)));
-typedef double f64x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kChooseWaves = 8;
-
-// How many of a lane's NL keys (in registers; NL == 0: n keys in LDS) reach t,
-// summed over the wave.
-template <int NL>
-__device__ __forceinline__ int count_from(const uint64_t (&x)[NL ? NL : 1], const uint64_t *kr,
-                                          int nk, int lane, uint64_t t) {
-    int n = 0;
-    if (NL) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) n += __popcll(__ballot(x[i] >= t));
-    } else {
-        for (int j = lane; j < nk + lane; j += 64)          // all lanes take part
-            n += __popcll(__ballot(j < nk && kr[j < nk ? j : 0] >= t));
-    }
-    return n;
-}
 
 // The `keep` highest of a query block's keys, by one wave: the largest
 // threshold that at least `keep` keys reach, bit by bit below the first bit in
-// which the highest and the lowest key differ (one ballot per 64 keys and bit;
-// it ends early when exactly `keep` reach it), then the numbers of the keys
-// above it in ascending order, equal ones from the lowest number up to the
-// count.
+// which the highest and the lowest key differ (one ballot per 64 keys and bit,
+// on the keys' upper words while the bit is one of theirs: a 64-bit compare
+// takes four times as long; it ends early when exactly `keep` reach it), then
+// the numbers of the keys above it in ascending order, equal ones from the
+// lowest number up to the count.  NL: a lane's keys in registers (nk <= 64 NL),
+// or 0: in LDS.
 template <int NL>
 __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, int keep, int lane,
                                        int32_t *out) {
@@ -109,44 +108,63 @@ __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, in
     if (NL)
 #pragma unroll
         for (int i = 0; i < NL; ++i) x[i] = 64 * i + lane < nk ? kr[64 * i + lane] : 0;
+    // f(the lane's key i, its chunk of 64) over all chunks, by all lanes; past nk: key 0
+    auto each = [&](auto f) {
+        if (NL) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) f(x[i], i);
+        } else {
+            for (int i = 0; 64 * i < nk; ++i) f(64 * i + lane < nk ? kr[64 * i + lane] : 0ull, i);
+        }
+    };
     uint64_t at = 1;                                         // keys >= at are taken,
     int ties = 0x7FFFFFFF;                                   // `ties` of those equal to it at most
     if (valid > keep) {
         uint64_t any = 0, all = ~0ull;                       // bits set in some / in every valid key
-        for (int j = lane; j < valid; j += 64) {
-            any |= kr[j];
-            all &= kr[j];
-        }
+        each([&](uint64_t y, int) {
+            any |= y;
+            all &= y ? y : ~0ull;
+        });
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) {
             any |= __shfl_xor(any, d);
             all &= __shfl_xor(all, d);
         }
         const uint64_t differ = any & ~all;
-        const int top = differ ? 63 - __builtin_clzll(differ) : -1;
-        at = top == 63 ? 0 : all & ~((2ull << (top < 0 ? 0 : top)) - 1);
-        if (top < 0) at = all;                               // all equal
+        int bit = differ ? 63 - __builtin_clzll(differ) : -1;
+        at = bit < 0 ? all : bit == 63 ? 0 : all & ~((2ull << bit) - 1);
         bool exact = false;
-        for (int bit = top; bit >= 0 && !exact; --bit) {
+        for (; bit >= 32 && !exact; --bit) {
+            const uint32_t t = (uint32_t)(at >> 32) | 1u << (bit - 32);
+            int n = 0;
+            each([&](uint64_t y, int) { n += __popcll(__ballot((uint32_t)(y >> 32) >= t)); });
+            if (n >= keep) at = (uint64_t)t << 32;
+            exact = n == keep;
+        }
+        for (; bit >= 0 && !exact; --bit) {
             const uint64_t t = at | 1ull << bit;
-            const int n = count_from<NL>(x, kr, nk, lane, t);
+            int n = 0;
+            each([&](uint64_t y, int) { n += __popcll(__ballot(y >= t)); });
             if (n >= keep) at = t;
             exact = n == keep;
         }
-        if (!exact) ties = at == ~0ull ? keep : keep - count_from<NL>(x, kr, nk, lane, at + 1);
+        if (!exact) {
+            int above = 0;
+            each([&](uint64_t y, int) { above += __popcll(__ballot(y > at)); });
+            ties = keep - above;
+        }
     }
     int n = 0;
     const uint64_t below = (1ull << lane) - 1;
-    for (int j = lane; j < nk + lane; j += 64) {
-        const uint64_t y = j < nk ? kr[j] : 0;
+    each([&](uint64_t y, int i) {
         const uint64_t equal = __ballot(y == at);
         const bool take = y > at || (y == at && __popcll(equal & below) < ties);
         const uint64_t taken = __ballot(take);
         const int pos = n + __popcll(taken & below);
-        if (take && pos < keep) out[pos] = j;
+        if (take && pos < keep) out[pos] = 64 * i + lane;
         n += __popcll(taken);
         ties -= __popcll(equal) < ties ? __popcll(equal) : ties;
-    }
+    });
     for (int p = n + lane; p < keep; p += 64) out[p] = -1;
 }
 
@@ -159,42 +177,48 @@ __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, in
 // The keys go to LDS, where a wave then chooses for each of its query blocks.
 template <int D>
 __global__ void __launch_bounds__(64 * kChooseWaves)
-block_choose_kernel(const double *__restrict__ qm, const double *__restrict__ km,
+block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
                     const int32_t *__restrict__ kv_len, AttnShape a, int R,
                     int32_t *__restrict__ blocks) {
     extern __shared__ uint64_t keys[];                       // [R][nk]
     constexpr int STEPS = D / 8;                             // pairs of 16x16x4 products
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t per = (a.nq + R - 1) / R;
-    const int64_t plane = blockIdx.x / per;
-    const int64_t i0 = (blockIdx.x - plane * per) * R;
+    const int64_t id = xcd_range(blockIdx.x, a.planes_q * per);   // a head's means in few L2s
+    const int64_t plane = id / per;
+    const int64_t i0 = (id - plane * per) * R;
     const int64_t b = plane / a.H, h = plane - b * a.H;
     const int64_t kplane = b * a.G + h / (a.H / a.G);
     const int nk = (int)a.nk;
     const int valid = (int)((valid_keys(kv_len, b, a.seq_k) + kKB - 1) / kKB);
     const int c = lane & 15, g = lane >> 4;
-    f64x2 qf[STEPS];
-    {
-        int64_t i = i0 + (c < R ? c : R - 1);
-        if (i >= a.nq) i = a.nq - 1;
-        const double *p = qm + (plane * a.nq + i) * D + 2 * g;
+    // Blocks past the end, or without a valid key, have no mean: what is read in
+    // their place is another one of the tile or what the workspace held, and is
+    // used for no key.
+    const f64x2 *kp = km + kplane * mean_tiles(a.nk) * (8 * D) + lane;
+    f64x2 qf[STEPS], kf[STEPS];
+    auto load_k = [&](int j0) {
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) qf[s] = *reinterpret_cast<const f64x2 *>(p + 8 * s);
+        for (int s = 0; s < STEPS; ++s) kf[s] = kp[(int64_t)(j0 >> 4) * (8 * D) + 64 * s];
+    };
+    if (16 * wave < valid) load_k(16 * wave);
+    {
+        const int64_t i = i0 + (c < R ? c : R - 1);
+        const f64x2 *p = qm + plane * mean_tiles(a.nq) * (8 * D) +
+                         mean_at<D>(i < a.nq ? i : a.nq - 1, g);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) qf[s] = p[64 * s];
     }
     for (int j0 = 16 * wave; j0 < nk; j0 += 16 * kChooseWaves) {
         const int j = j0 + c;
         f64x4 acc = {};
         if (j0 < valid) {                                    // uniform
-            // blocks without a valid key have no mean: read another, never used
-            const double *p = km + (kplane * nk + (j < valid ? j : valid - 1)) * D + 2 * g;
-            f64x2 kf[STEPS];
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const f64x2 *>(p + 8 * s);
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].x, kf[s].x, acc, 0, 0, 0);
                 acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].y, kf[s].y, acc, 0, 0, 0);
             }
+            if (j0 + 16 * kChooseWaves < valid) load_k(j0 + 16 * kChooseWaves);
         }
         if (j < nk)
 #pragma unroll
@@ -216,21 +240,30 @@ block_choose_kernel(const double *__restrict__ qm, const double *__restrict__ km
 
 namespace {
 
+// 64-bit means of a side, its blocks in tiles of 16.
+size_t means_bytes(int64_t planes, int64_t blocks, int D) {
+    return align256((size_t)planes * (size_t)mean_tiles(blocks) * 16 * D * 8);
+}
+
 // Query blocks per workgroup: their keys fit 64 KB of LDS (two workgroups per
-// compute unit), or 128 KB for the longest sequences.
-int choose_rows(int64_t nk) { return nk <= 512 ? 16 : nk <= 1024 ? 8 : 4; }
+// compute unit; 128 KB for the longest sequences).  The matrix instruction
+// takes 16 rows whatever R is: with 8 where 16 leave compute units without a
+// workgroup, 12 heads of 256 x 512 blocks took 34 us instead of 24.
+int choose_rows(const AttnShape &a) {
+    const int R = a.nk <= 512 ? 16 : a.nk <= 1024 ? 8 : 4;
+    return (int)(R < a.nq ? R : a.nq);
+}
 
 template <int D>
 hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, const AttnShape &a,
                   int32_t *blocks, void *ws, hipStream_t stream) {
-    double *qm = static_cast<double *>(ws);
-    double *km = reinterpret_cast<double *>(static_cast<char *>(ws) +
-                                            align256((size_t)a.planes_q * a.nq * D * 8));
+    f64x2 *qm = static_cast<f64x2 *>(ws);
+    f64x2 *km = reinterpret_cast<f64x2 *>(static_cast<char *>(ws) + means_bytes(a.planes_q, a.nq, D));
     block_means_kernel<D><<<(unsigned)(a.planes_q * a.nq + a.planes_k * a.nk), 256, 0, stream>>>(
         q, k, kv_len, a, qm, km);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int R = (int)(choose_rows(a.nk) < a.nq ? choose_rows(a.nk) : a.nq);
+    const int R = choose_rows(a);
     const unsigned grid = (unsigned)(a.planes_q * ((a.nq + R - 1) / R));
     block_choose_kernel<D><<<grid, 64 * kChooseWaves, (size_t)R * a.nk * 8, stream>>>(
         qm, km, kv_len, a, R, blocks);
@@ -240,8 +273,7 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, c
 }  // namespace
 
 size_t select_workspace(const AttnShape &a) {
-    return align256((size_t)a.planes_q * a.nq * a.D * 8) +
-           align256((size_t)a.planes_k * a.nk * a.D * 8);
+    return means_bytes(a.planes_q, a.nq, a.D) + means_bytes(a.planes_k, a.nk, a.D);
 }
 
 hipError_t launch_select_blocks(const uint16_t *q, const uint16_t *k, const int32_t *kv_len,

@@ -45,13 +45,6 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4));
 }
 
-// Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a contiguous
-// range of the tiles, so that tiles sharing operands share its L2.
-__device__ __forceinline__ int64_t xcd_range(int64_t b, int64_t n) {
-    const int64_t x = b & 7, q = n >> 3, r = n & 7;
-    return x * q + (x < r ? x : r) + (b >> 3);
-}
-
 template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_;          // tokens, output channels

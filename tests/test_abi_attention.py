@@ -224,8 +224,8 @@ def test_sparse_attention_null_shape_and_empty(fn):
 
 
 def test_sparse_attention_workspace_sizes():
-    # 64-bit means of 2 x 4 x 2 query and 2 x 2 x 5 key blocks of 128 columns
-    means = 2 * 4 * 2 * 128 * 8 + 2 * 2 * 5 * 128 * 8
+    # 64-bit means of 2 x 4 x 2 query and 2 x 2 x 5 key blocks of 128 columns, in tiles of 16
+    means = 2 * 4 * 16 * 128 * 8 + 2 * 2 * 16 * 128 * 8
     assert bdt.svdq_select_blocks_workspace_bytes(_shape()) == means
     assert bdt.svdq_sparse_attention_workspace_bytes(_shape()) >= means + 2 * 4 * 2 * 3 * 4
     assert bdt.svdq_block_attention_workspace_bytes(_shape(batch=64, seq_q=4096)) == 0
