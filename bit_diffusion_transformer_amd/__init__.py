@@ -252,6 +252,21 @@ def mlp(X, up: dict, down: dict, act: int = ACT_GELU,
     return Y
 
 
+def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamma_q, gamma_k,
+              eps: float, cos_t, sin_t, keep: int, first: int = 0,
+              kv_len: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = out(sparse_attention(qkv(X))): the attention half of a block on two W4A4 layers
+    (dicts with lam, L1, qw, sw, L2, bias), through svdq_linear_qkv, svdq_sparse_attention and
+    svdq_linear.  X bf16 [M, K], M = B seq; cos_t, sin_t from rope_tables; keep, first and
+    kv_len as for sparse_attention."""
+    Q, Kt, V = linear_qkv(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"],
+                          qkv.get("bias"), heads, head_dim, seq, gamma_q, gamma_k, eps, cos_t,
+                          sin_t)
+    A = sparse_attention(Q, Kt, V, keep, first=first, kv_len=kv_len)
+    return linear(A.view(X.shape[0], heads * head_dim), out["lam"], out["L1"], out["qw"],
+                  out["sw"], out["L2"], out.get("bias"))
+
+
 def group_sums(qa, sa, qw, sw, M: int, N: int, m0: int, n0: int, tm: int,
                tn: int) -> torch.Tensor:
     """Exact per-group int32 sums of a block (test hook, through the GEMM's own tile code)

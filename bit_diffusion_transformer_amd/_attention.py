@@ -7,7 +7,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from ._binding import QkvEpilogue, qkv_epilogue
+from ._binding import QkvEpilogue
 from ._tensors import (BF16, Entries, F32, F32T, I32, I32T, I64, P, SZ, expect, on, one_device,
                        ptr, scratch, stream_ptr)
 
@@ -108,10 +108,9 @@ def rope_tables(pos: torch.Tensor, dims: Sequence[int], theta=10000.0):
     qkv_norm_rope take them.  Axis a turns dims[a] elements of each head; theta: one number,
     or one per axis."""
     axes = rope_axes(dims, theta)
-    S = expect(pos, "pos", F32, (None, axes.axes)).shape[0]
+    S = expect(pos, "pos", F32, (None, axes.axes))[0]
     dev = one_device(pos=pos)
-    t = torch.empty((2, S, sum(axes.dims) // 2), dtype=torch.float32, device=dev)
-    cos_t, sin_t = t.unbind(0)
+    cos_t, sin_t = torch.empty((2, S, sum(axes.dims) // 2), dtype=torch.float32, device=dev).unbind(0)
     with on(dev):
         svdq_rope_tables(pos, S, axes, cos_t, sin_t)
     return cos_t, sin_t
@@ -122,7 +121,7 @@ def qkv_norm_rope(qkv: torch.Tensor, heads: int, head_dim: int, seq: int, gamma_
     """A written projection bf16 [M, 3 heads head_dim] -> (Q, K, V) bf16 [M/seq, heads, seq,
     head_dim], Q and K with their RMS norm (gamma None: without) and rotary turn."""
     N = 3 * heads * head_dim
-    M = expect(qkv, "qkv", BF16, (None, N)).shape[0]
+    M = expect(qkv, "qkv", BF16, (None, N))[0]
     for what, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
         if g is not None:
             expect(g, what, BF16, (head_dim,))
@@ -133,15 +132,17 @@ def qkv_norm_rope(qkv: torch.Tensor, heads: int, head_dim: int, seq: int, gamma_
     dev = one_device(qkv=qkv, gamma_q=gamma_q, gamma_k=gamma_k, cos_t=cos_t, sin_t=sin_t)
     out = torch.empty((3, M // seq, heads, seq, head_dim), dtype=torch.bfloat16, device=dev)
     Q, K, V = out.unbind(0)
-    epi = qkv_epilogue(heads, head_dim, seq, gamma_q, gamma_k, eps, cos_t, sin_t, Q, K, V)
+    at, each = out.data_ptr(), M * heads * head_dim * 2
+    epi = QkvEpilogue(heads, head_dim, seq, ptr(gamma_q), ptr(gamma_k), eps, ptr(cos_t),
+                      ptr(sin_t), at, at + each, at + 2 * each)
     with on(dev):
         svdq_qkv_norm_rope(qkv, M, epi)
     return Q, K, V
 
 
 def _shape(q, k, kv_len, keep, first) -> AttentionShape:
-    B, H, Sq, D = expect(q, "q", BF16, (None, None, None, None)).shape
-    _, G, Sk, _ = expect(k, "k", BF16, (B, None, None, D)).shape
+    B, H, Sq, D = expect(q, "q", BF16, (None, None, None, None))
+    _, G, Sk, _ = expect(k, "k", BF16, (B, None, None, D))
     if kv_len is not None:
         expect(kv_len, "kv_len", I32, (B,))
     return AttentionShape(B, Sq, Sk, H, G, D, keep, first)

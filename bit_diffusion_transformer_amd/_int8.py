@@ -55,7 +55,7 @@ def svdq_i8_linear(X, lam, qw, sw, bias, act, M, N, K, Y, workspace, ws_bytes, s
 
 def i8_pack_weights(W: torch.Tensor):
     """fp32 weight [N, K] -> (qw int8 [N, K], sw fp32 [N])."""
-    N, K = expect(W, "W", F32, (None, None)).shape
+    N, K = expect(W, "W", F32, (None, None))
     dev = one_device(W=W)
     qw = torch.empty((N, K), dtype=torch.int8, device=dev)
     sw = torch.empty(N, dtype=torch.float32, device=dev)
@@ -66,7 +66,7 @@ def i8_pack_weights(W: torch.Tensor):
 
 def i8_quantize_act(X: torch.Tensor, lam: Optional[torch.Tensor] = None):
     """X bf16 [M, K], smoothed by 1 / lam fp32 [K] if given -> (qa int8 [M, K], sa fp32 [M])."""
-    M, K = expect(X, "X", BF16, (None, None)).shape
+    M, K = expect(X, "X", BF16, (None, None))
     if lam is not None:
         expect(lam, "lam", F32, (K,))
     dev = one_device(X=X, lam=lam)
@@ -78,7 +78,7 @@ def i8_quantize_act(X: torch.Tensor, lam: Optional[torch.Tensor] = None):
 
 
 def _weight(qw, sw, bias, K):
-    N = expect(qw, "qw", I8, (None, K)).shape[0]
+    N = expect(qw, "qw", I8, (None, K))[0]
     expect(sw, "sw", F32, (N,))
     if bias is not None:
         expect(bias, "bias", BF16, (N,))
@@ -88,7 +88,7 @@ def _weight(qw, sw, bias, K):
 def i8_gemm(qa, sa, qw, sw, bias=None, act: int = ACT_NONE,
             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """act((qa qw^T) sa sw + bias) -> Y bf16 [M, N]; codes in [-127, 127]."""
-    M, K = expect(qa, "qa", I8, (None, None)).shape
+    M, K = expect(qa, "qa", I8, (None, None))
     expect(sa, "sa", F32, (M,))
     N = _weight(qw, sw, bias, K)
     dev = one_device(qa=qa, sa=sa, qw=qw, sw=sw, bias=bias)
@@ -104,7 +104,7 @@ def i8_linear(X, lam, qw, sw, bias=None, act: int = ACT_NONE,
               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The whole 8-bit layer: X bf16 [M, K] -> Y bf16 [M, N] (lam fp32 [K] or None; qw, sw from
     i8_pack_weights, or int8 codes in [-127, 127] and channel scales made elsewhere)."""
-    M, K = expect(X, "X", BF16, (None, None)).shape
+    M, K = expect(X, "X", BF16, (None, None))
     if lam is not None:
         expect(lam, "lam", F32, (K,))
     N = _weight(qw, sw, bias, K)

@@ -13,18 +13,25 @@ from ._binding import _check, load_library
 _SAME = contextlib.nullcontext()
 
 
-def expect(t: torch.Tensor, what: str, dtypes, shape) -> torch.Tensor:
-    """A contiguous tensor of one of `dtypes` and of `shape` (None entries are free)."""
+def expect(t: torch.Tensor, what: str, dtypes, shape) -> torch.Size:
+    """The shape of `t`, a contiguous tensor of one of `dtypes` and of `shape` (None entries
+    are free)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a tensor, got %s" % (what, type(t).__name__))
     if t.dtype not in dtypes:
         raise TypeError("%s: expected %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    got = t.shape
+    fits = len(got) == len(shape)
+    if fits:
+        for n, w in zip(got, shape):
+            if w is not None and w != n:
+                fits = False
+    if not fits:
         raise ValueError("%s: expected shape %s, got %s"
-                         % (what, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
+                         % (what, tuple("*" if w is None else w for w in shape), tuple(got)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    return t
+    return got
 
 
 BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 or its bit patterns
@@ -57,12 +64,19 @@ def ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle alone; torch.cuda.current_stream makes an object of it, which
+# takes as long as half a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def stream_ptr(stream=None):
-    if stream is None:
-        if not torch.cuda.is_available():
-            return None
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        return None
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
