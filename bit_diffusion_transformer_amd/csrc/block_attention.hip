@@ -13,7 +13,7 @@
 // while the current one is used); K is read in 16-byte pieces, V through the
 // transposing 8-byte LDS read.
 #include "attention_internal.h"
-#include "svdq_device.h"
+#include "svdq_wave.h"
 
 #include <type_traits>
 
@@ -25,11 +25,6 @@ constexpr int kQB = SVDQ_QUERY_BLOCK, kKB = SVDQ_KEY_BLOCK;
 constexpr int kMaxList = SVDQ_MAX_KEYS / SVDQ_KEY_BLOCK;
 
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
-
-// Every vector-memory instruction of this wave done and its LDS reads returned.
-__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x7 << 4); }
 
 // c plus the two bf16 values of x (products with one): the sum of the weights as
 // they enter the second product, rounded, in half the instructions.
@@ -207,8 +202,8 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
     auto block = [&](int i, auto buffer) {
         constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
         const int n0 = __builtin_amdgcn_readfirstlane(lds.list[i]) * kKB;
-        wait_all();
-        barrier();
+        wait_loads<0>();
+        wave_barrier_all();
         if (i + 1 < last) issue(i + 1, std::integral_constant<int, 1 - BUF>());
         if (!active) return;
         f32x16 s[2] = {f32x16{}, f32x16{}};

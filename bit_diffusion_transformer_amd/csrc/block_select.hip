@@ -6,7 +6,7 @@
 // another block there than by the definition.  The work in 64 bits is small
 // (one product of D per pair of blocks, 1/8192 of the pairs of rows).
 #include "attention_internal.h"
-#include "svdq_device.h"
+#include "svdq_wave.h"
 
 namespace svdq {
 

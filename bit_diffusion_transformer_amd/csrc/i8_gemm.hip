@@ -11,7 +11,7 @@
 // (exact: K <= 2^17).  The epilogue scales in fp32, adds the bias, applies
 // the activation and rounds once.
 #include "i8_internal.h"
-#include "svdq_device.h"
+#include "svdq_wave.h"
 
 #include <type_traits>
 
@@ -35,15 +35,6 @@ __device__ __forceinline__ i32x16 mfma_i8_32x32x32(i32x4 a, i32x4 b, i32x16 c) {
 // rows of one segment touch 8 distinct slots (all banks of a 128-byte pass),
 // any 16 consecutive rows 16 distinct 16-byte groups of 256 bytes.
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
-
-// At most `n` vector-memory instructions of this wave in flight, and all its
-// LDS reads returned.
-template <int n>
-__device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4));
-}
 
 template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
 struct Tile {
@@ -131,41 +122,58 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
 #pragma unroll
         for (int j = 0; j < T::MB; ++j) acc[i][j] = i32x16{};
 
-    auto steps = [&](const uint8_t *st, auto count) {
+    // Fragments of one k step, double-buffered: step kk + 1 is read while the
+    // products of step kk run.  The barrier that hands a stage's buffer back sits
+    // before its last step's products, whose operands are in registers by then:
+    // they cover the barrier and the first reads of the next stage.
+    struct Frags {
+        i32x4 a[T::NB], b[T::MB];
+    } f[2];
+    auto load = [&](Frags &x, const uint8_t *st, int kk) {
 #pragma unroll
-        for (int kk = 0; kk < decltype(count)::value; ++kk) {
-            i32x4 a[T::NB], b[T::MB];
+        for (int i = 0; i < T::NB; ++i)
+            x.a[i] = *reinterpret_cast<const i32x4 *>(st + a_at[kk] + i * 32 * kRow);
 #pragma unroll
-            for (int i = 0; i < T::NB; ++i)
-                a[i] = *reinterpret_cast<const i32x4 *>(st + a_at[kk] + i * 32 * kRow);
+        for (int j = 0; j < T::MB; ++j)
+            x.b[j] = *reinterpret_cast<const i32x4 *>(st + b_at[kk] + j * 32 * kRow);
+    };
+    auto mul = [&](const Frags &x) {
 #pragma unroll
-            for (int j = 0; j < T::MB; ++j)
-                b[j] = *reinterpret_cast<const i32x4 *>(st + b_at[kk] + j * 32 * kRow);
+        for (int i = 0; i < T::NB; ++i)
 #pragma unroll
-            for (int i = 0; i < T::NB; ++i)
-#pragma unroll
-                for (int j = 0; j < T::MB; ++j) acc[i][j] = mfma_i8_32x32x32(a[i], b[j], acc[i][j]);
-        }
+            for (int j = 0; j < T::MB; ++j) acc[i][j] = mfma_i8_32x32x32(x.a[i], x.b[j], acc[i][j]);
     };
 
 #pragma unroll
-    for (int s = 0; s < T::NBUF - 1; ++s)
+    for (int s = 0; s < T::NBUF; ++s)
         if (s < ns) issue(s);
+    if (ns >= T::NBUF) wait_loads<(T::NBUF - 1) * T::LOADS>();
+    else wait_loads<0>();
+    wave_barrier_all();
+    load(f[0], lds, 0);
     for (int s = 0; s < nf; ++s) {
-        // stage s has landed when at most the younger stages in flight remain
-        if (s + T::NBUF - 1 <= ns) wait_loads<(T::NBUF - 2) * T::LOADS>();
+        const uint8_t *st = lds + (s % T::NBUF) * T::STAGE;
+        load(f[1], st, 1);
+        mul(f[0]);
+        load(f[0], st, 2);
+        mul(f[1]);
+        load(f[1], st, 3);
+        mul(f[0]);
+        // stage s + 1 has landed when at most the younger stages remain in flight
+        if (s + T::NBUF <= ns) wait_loads<(T::NBUF - 2) * T::LOADS>();
         else wait_loads<0>();
-        barrier();
-        if (s + T::NBUF - 1 < ns) issue(s + T::NBUF - 1);
-        steps(lds + (s % T::NBUF) * T::STAGE, std::integral_constant<int, 4>());
+        wave_barrier_all();
+        if (s + T::NBUF < ns) issue(s + T::NBUF);
+        if (s + 1 < ns) load(f[0], lds + ((s + 1) % T::NBUF) * T::STAGE, 0);
+        mul(f[1]);
     }
     if (half) {
-        wait_loads<0>();
-        barrier();
-        steps(lds + (nf % T::NBUF) * T::STAGE, std::integral_constant<int, 2>());
+        load(f[1], lds + (nf % T::NBUF) * T::STAGE, 1);
+        mul(f[0]);
+        mul(f[1]);
     }
     wait_loads<0>();
-    barrier();                                       // the ring becomes the output staging
+    wave_barrier_all();                              // the ring becomes the output staging
 
     // Epilogue: lane l holds, of token column l % 32 of each block, channels
     // 8 q + 4 (l / 32) .. + 3 for q = 0 .. 3.  The wave stages [token][channel]

@@ -90,24 +90,6 @@ __device__ __forceinline__ f32x16 mfma_mxfp4_32x32x64(u32x4 a, uint32_t sa, u32x
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// ---------------------------------------------------------------- workgroup order
-
-// Consecutive workgroups go to the 8 XCDs in turn.  The b-th of n, mapped so that
-// each XCD gets a contiguous range, whose operands its L2 then holds.
-__device__ __forceinline__ int64_t xcd_range(int64_t b, int64_t n) {
-    const int64_t x = b & 7, q = n >> 3, r = n & 7;
-    return x * q + (x < r ? x : r) + (b >> 3);
-}
-
-// ---------------------------------------------------------------- LDS copies
-
-// 16 bytes per lane from global memory straight into LDS: lane l's bytes go to
-// dst + 16 l (dst uniform).  (A function of its own, not a template: the host
-// pass drops a kernel template that names this builtin.)
-__device__ __forceinline__ void copy16_to_lds(const void *src, void *dst) {
-    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-}
-
 // ---------------------------------------------------------------- GELU
 
 // GELU, erf form: 0.5 x (1 + erf(x / sqrt 2)), with erf from the rational
