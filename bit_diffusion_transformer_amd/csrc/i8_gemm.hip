@@ -202,7 +202,7 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     y[e] = (float)acc[i][j][4 * q + e] * (a * w[e]) + b[e];
-                    if (act) y[e] = gelu_erf(y[e]);
+                    if (act) y[e] = gelu_exp2(y[e]);
                 }
                 const int seg = (4 * i + q) ^ (row & (T::SEGS - 1));
                 *reinterpret_cast<u32x2 *>(out + (row * T::SEGS + seg) * 16 + 8 * h) =
@@ -217,7 +217,8 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
         const int row = it * ROWS + lane / T::SEGS, sl = lane % T::SEGS;
         const u32x4 y = *reinterpret_cast<const u32x4 *>(out + (row * T::SEGS + (sl ^ (row & (T::SEGS - 1)))) * 16);
         const int64_t m = mw + row, n = nw + 8 * sl;
-        if (m < M && n < N) *reinterpret_cast<u32x4 *>(Y + m * N + n) = y;
+        if (m < M && n < N)   // not read again here: past the L2, whose room the operands use
+            __builtin_nontemporal_store(y, reinterpret_cast<u32x4 *>(Y + m * N + n));
     }
 }
 

@@ -126,6 +126,26 @@ def test_gemm(M, N, K, act):
     assert torch.equal(Y, bdt.i8_gemm(qa, sa, qw, sw, bias, act))     # deterministic
 
 
+@pytest.mark.parametrize("M", [4, 300, 4096])
+def test_gelu_epilogue_accuracy(M):
+    """One product of 127 127 per output, scaled to a grid of pre-activations over -12 .. 12, the
+    tails and zero, on every tile size: half a bf16 step and 4e-7 |x| of the exact erf form
+    (the pre-activation itself is off by at most 2 2^-24 of it, and GELU's slope is below 1.13)."""
+    K, N = 64, 4096
+    x = torch.cat([torch.linspace(-12, 12, N - 40, dtype=torch.float64, device=DEV),
+                   torch.logspace(-30, 30, 20, dtype=torch.float64, device=DEV),
+                   -torch.logspace(-30, 30, 20, dtype=torch.float64, device=DEV)])
+    qa = torch.zeros(M, K, dtype=torch.int8, device=DEV)
+    qw = torch.zeros(N, K, dtype=torch.int8, device=DEV)
+    qa[:, 0], qw[:, 0] = 127, 127
+    sw = (x / 16129).float()
+    Y = bdt.i8_gemm(qa, torch.ones(M, device=DEV), qw, sw, None, 1).double()
+    pre = sw.double() * 16129
+    ref = pre * torch.special.erfc(-pre / 2 ** 0.5) / 2
+    tol = 2.0 ** -8 * ref.abs() + (4e-7 + 1.13 * 2 * 2.0 ** -24) * pre.abs()
+    assert bool(((Y - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("M", [1, 16, 200, 3000])
 def test_gemm_largest_sums_are_exact(M):
     """Every code 127 at the longest K: S = 127^2 2^17, below 2^31 by less than 2 %; scales of
