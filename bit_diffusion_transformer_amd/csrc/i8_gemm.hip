@@ -36,31 +36,40 @@ __device__ __forceinline__ i32x16 mfma_i8_32x32x32(i32x4 a, i32x4 b, i32x16 c) {
 // any 16 consecutive rows 16 distinct 16-byte groups of 256 bytes.
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-template <int BM_, int BN_, int WM_, int WN_, int NBUF_>
+// WM x WN waves cover a tile; KS such groups share its stages of K in turn (stage
+// s goes to group s % KS), each with a ring of its own, and add their sums at
+// the end.
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int KS_ = 1>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_;          // tokens, output channels
     static constexpr int WM = WM_, WN = WN_;          // waves along each
     static constexpr int NBUF = NBUF_;                // stages in the ring
-    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int KS = KS_;                    // groups along K
+    static constexpr int WAVES = WM * WN;             // of a group
+    static constexpr int THREADS = 64 * WAVES * KS;
     static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks per wave
     static constexpr int STAGE = (BM + BN) * kRow;
     static constexpr int CW = BN / 8 / WAVES;                    // copies per wave and stage, W
     static constexpr int LOADS = CW + BM / 8 / WAVES;            // and both operands
     static constexpr int SEGS = NB * 4;               // 16-byte segments of a staged output row
     static constexpr int OUT = MB * 32 * SEGS * 16;   // a wave's staged output
-    static constexpr int LDS = NBUF * STAGE > WAVES * OUT ? NBUF * STAGE : WAVES * OUT;
+    static constexpr int SUMS = (KS - 1) * BM * BN * 4;          // the other groups' sums
+    static constexpr int RING = NBUF * STAGE;                    // of a group
+    static constexpr int LDS = KS * RING > SUMS + WAVES * OUT ? KS * RING : SUMS + WAVES * OUT;
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole copies per wave");
     static_assert((SEGS & (SEGS - 1)) == 0, "the staging swizzle");
 };
 
 template <class T>
-__global__ void __launch_bounds__(T::THREADS, T::WAVES == 8 ? 2 : 1)
+__global__ void __launch_bounds__(T::THREADS, T::WAVES == 8 ? 2 : T::KS * T::WAVES / 4 > 1 ? T::KS * T::WAVES / 4 : 1)
 i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
                const int8_t *__restrict__ qw, const float *__restrict__ sw,
                const uint16_t *__restrict__ bias, int act, int64_t M, int64_t N, int64_t K,
                uint16_t *__restrict__ Y) {
     __shared__ __align__(1024) uint8_t lds[T::LDS];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = wid % T::WAVES, group = wid / T::WAVES;
+    uint8_t *const ring = lds + group * T::RING;
     const int64_t nbm = (M + T::BM - 1) / T::BM, nbn = (N + T::BN - 1) / T::BN;
     int64_t m0, n0;
     {
@@ -90,8 +99,8 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
     const int nf = (int)(K / kRow);                  // whole stages
     const bool half = (K & 64) != 0;                 // then one of 64 bytes
     const int ns = nf + (half ? 1 : 0);
-    auto issue = [&](int s) {
-        uint8_t *st = lds + (s % T::NBUF) * T::STAGE + wave * 1024;
+    auto issue = [&](int s, int slot) {
+        uint8_t *st = ring + slot * T::STAGE + wave * 1024;
         const int64_t g = (int64_t)s * kRow;
         const bool last = s == nf;
 #pragma unroll
@@ -144,64 +153,114 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
             for (int j = 0; j < T::MB; ++j) acc[i][j] = mfma_i8_32x32x32(x.a[i], x.b[j], acc[i][j]);
     };
 
+    // The group's i-th stage is stage group + KS i; every group runs `turns` of
+    // them, so that all meet at every barrier.
+    const int turns = (ns + T::KS - 1) / T::KS;
+    auto stage = [&](int i) { return T::KS * i + group; };
 #pragma unroll
-    for (int s = 0; s < T::NBUF; ++s)
-        if (s < ns) issue(s);
-    if (ns >= T::NBUF) wait_loads<(T::NBUF - 1) * T::LOADS>();
+    for (int i = 0; i < T::NBUF; ++i)
+        if (stage(i) < ns) issue(stage(i), i);
+    if (stage(T::NBUF - 1) < ns) wait_loads<(T::NBUF - 1) * T::LOADS>();
     else wait_loads<0>();
     wave_barrier_all();
-    load(f[0], lds, 0);
-    for (int s = 0; s < nf; ++s) {
-        const uint8_t *st = lds + (s % T::NBUF) * T::STAGE;
-        load(f[1], st, 1);
-        mul(f[0]);
-        load(f[0], st, 2);
-        mul(f[1]);
-        load(f[1], st, 3);
-        mul(f[0]);
-        // stage s + 1 has landed when at most the younger stages remain in flight
-        if (s + T::NBUF <= ns) wait_loads<(T::NBUF - 2) * T::LOADS>();
+    if (T::KS == 1 || group < ns) load(f[0], ring, 0);
+    for (int i = 0; T::KS == 1 ? i < nf : i < turns; ++i) {
+        const uint8_t *st = ring + (i % T::NBUF) * T::STAGE;
+        if (T::KS == 1 || stage(i) < nf) {
+            load(f[1], st, 1);
+            mul(f[0]);
+            load(f[0], st, 2);
+            mul(f[1]);
+            load(f[1], st, 3);
+            mul(f[0]);
+        } else if (stage(i) < ns) {                  // the 64-byte stage
+            load(f[1], st, 1);
+            mul(f[0]);
+        }
+        // the next stage has landed when at most the younger ones remain in flight
+        if (stage(i + T::NBUF - 1) < ns) wait_loads<(T::NBUF - 2) * T::LOADS>();
         else wait_loads<0>();
         wave_barrier_all();
-        if (s + T::NBUF < ns) issue(s + T::NBUF);
-        if (s + 1 < ns) load(f[0], lds + ((s + 1) % T::NBUF) * T::STAGE, 0);
-        mul(f[1]);
+        if (stage(i + T::NBUF) < ns) issue(stage(i + T::NBUF), i % T::NBUF);
+        if (stage(i + 1) < ns) load(f[0], ring + ((i + 1) % T::NBUF) * T::STAGE, 0);
+        if (T::KS == 1 || stage(i) < ns) mul(f[1]);
     }
-    if (half) {
-        load(f[1], lds + (nf % T::NBUF) * T::STAGE, 1);
+    if (T::KS == 1 && half) {
+        load(f[1], ring + (nf % T::NBUF) * T::STAGE, 1);
         mul(f[0]);
         mul(f[1]);
     }
     wait_loads<0>();
-    wave_barrier_all();                              // the ring becomes the output staging
+    wave_barrier_all();                              // the rings become sums and output staging
+    if (T::KS > 1) {
+        auto part = [&](int g, int i, int j, int q) {
+            return reinterpret_cast<i32x4 *>(
+                lds + ((((g - 1) * T::WAVES + wave) * T::NB + i) * T::MB + j) * 4096 + q * 1024 + lane * 16);
+        };
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::MB; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *part(group, i, j, q) = i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                      acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+        wait_loads<0>();
+        wave_barrier_all();
+        if (group > 0) return;
+        for (int g = 1; g < T::KS; ++g)
+#pragma unroll
+            for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::MB; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const i32x4 x = *part(g, i, j, q);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += x[e];
+                    }
+    }
 
     // Epilogue: lane l holds, of token column l % 32 of each block, channels
     // 8 q + 4 (l / 32) .. + 3 for q = 0 .. 3.  The wave stages [token][channel]
     // bf16 rows in its own part of the LDS and stores them as 16-byte segments.
-    uint8_t *out = lds + wave * T::OUT;
+    uint8_t *out = lds + T::SUMS + wave * T::OUT;
     const int64_t nw = n0 + wn * T::NB * 32, mw = m0 + wm * T::MB * 32;
     const int h = lane >> 5;
+    // Every scale and bias first, in one batch of loads (N % 8 == 0: four channels
+    // are in or out together; those past N re-read the last four, never stored).
+    f32x4 w[T::NB][4];
+    u32x2 c[T::NB][4];
+    float a[T::MB];
+#pragma unroll
+    for (int i = 0; i < T::NB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            int64_t n = nw + 32 * i + 8 * q + 4 * h;
+            n = n < N ? n : N - 4;
+            w[i][q] = *reinterpret_cast<const f32x4 *>(sw + n);
+            c[i][q] = bias ? *reinterpret_cast<const u32x2 *>(bias + n) : u32x2{};
+        }
+#pragma unroll
+    for (int j = 0; j < T::MB; ++j) {
+        const int64_t m = mw + 32 * j + (lane & 31);
+        a[j] = sa[m < M ? m : M - 1];
+    }
 #pragma unroll
     for (int j = 0; j < T::MB; ++j) {
         const int row = 32 * j + (lane & 31);
-        const int64_t m = mw + row;
-        const float a = m < M ? sa[m] : 0.0f;
 #pragma unroll
         for (int i = 0; i < T::NB; ++i) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t n = nw + 32 * i + 8 * q + 4 * h;
-                f32x4 w = {};
-                u32x2 c = {};
-                if (n < N) {                          // N % 8 == 0: four in or four out
-                    w = *reinterpret_cast<const f32x4 *>(sw + n);
-                    if (bias) c = *reinterpret_cast<const u32x2 *>(bias + n);
-                }
-                const float b[4] = {bf16_lo(c.x), bf16_hi(c.x), bf16_lo(c.y), bf16_hi(c.y)};
+                const float b[4] = {bf16_lo(c[i][q].x), bf16_hi(c[i][q].x), bf16_lo(c[i][q].y),
+                                    bf16_hi(c[i][q].y)};
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[e] = (float)acc[i][j][4 * q + e] * (a * w[e]) + b[e];
+                    y[e] = (float)acc[i][j][4 * q + e] * (a[j] * w[i][q][e]) + b[e];
                     if (act) y[e] = gelu_exp2(y[e]);
                 }
                 const int seg = (4 * i + q) ^ (row & (T::SEGS - 1));
@@ -226,8 +285,11 @@ i8_gemm_kernel(const int8_t *__restrict__ qa, const float *__restrict__ sa,
 // (channels), 32 MB x 64 each; one workgroup per compute unit.
 template <int BM>
 using Tall = Tile<BM, 256, 2, 4, 2>;
-typedef Tile<128, 128, 2, 2, 2> Mid;
-typedef Tile<64, 64, 2, 2, 4> Small;
+typedef Tile<128, 128, 2, 2, 4> Mid;          // one per compute unit, three stages ahead
+typedef Tile<128, 64, 2, 2, 3> Half;          // two per compute unit
+typedef Tile<64, 64, 2, 2, 4> Small;          // two per compute unit
+typedef Tile<32, 64, 1, 2, 3, 4> Few;         // few tiles: K shared by four groups
+typedef Tile<32, 32, 1, 1, 4, 4> Fewest;
 
 template <class T>
 int64_t tiles(int64_t M, int64_t N) {
@@ -252,23 +314,31 @@ hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, c
             qa, sa, qw, sw, bias, act, M, N, K, Y);
         return hipGetLastError();
     };
-    if (tiles<Tall<256>>(M, N) >= cus) {
-        // The height with the shortest time for the whole rounds of compute
-        // units that its tiles take, a tile's time taken as its height + 16.
-        int best = 0;
-        int64_t least = 0;
-        for (int bm = 128; bm <= 320; bm += 64) {
-            const int64_t n = (M + bm - 1) / bm * ((N + 255) / 256);
-            const int64_t cost = (n + cus - 1) / cus * (bm + 16);
-            if (!best || cost < least) best = bm, least = cost;
-        }
-        if (best == 128) return run(Tall<128>());
-        if (best == 192) return run(Tall<192>());
-        if (best == 256) return run(Tall<256>());
-        return run(Tall<320>());
+    // The smaller tiles while they fit the compute units once (K shared by four
+    // groups of waves) or twice; then larger ones, whose operands are read less
+    // often.  Measured with K = 4096 and N = 4096 in us, at M = 1, 64, 128, 333,
+    // 512, 777, 1024: Fewest 7.3, 8.2, 14, ..; Few 8.8, 9.4, 9.9, 26, ..; Small 11,
+    // 11, 12, 15, 17, 33, 38; Half 17, 17, 17, 18, 19, 25, 30; Mid 22, 22, 22, 23,
+    // 24, 27, 28.
+    if (tiles<Fewest>(M, N) <= cus) return run(Fewest());
+    if (tiles<Few>(M, N) <= cus) return run(Few());
+    if (tiles<Small>(M, N) <= 2 * cus) return run(Small());
+    if (4 * tiles<Mid>(M, N) < 3 * cus) return run(Half());
+    if (tiles<Mid>(M, N) <= cus) return run(Mid());
+    // Tall tiles: the height with the shortest time for the whole rounds of
+    // compute units that its tiles take; a round costs its rows and, for filling
+    // the ring and the epilogue, as much as 112 rows at K = 4096.
+    int best = 0;
+    int64_t least = 0;
+    for (int bm = 128; bm <= 320; bm += 64) {
+        const int64_t n = (M + bm - 1) / bm * ((N + 255) / 256);
+        const int64_t cost = (n + cus - 1) / cus * (bm * K + 112 * 4096);
+        if (!best || cost < least) best = bm, least = cost;
     }
-    if (tiles<Mid>(M, N) >= cus) return run(Mid());
-    return run(Small());
+    if (best == 128) return run(Tall<128>());
+    if (best == 192) return run(Tall<192>());
+    if (best == 256) return run(Tall<256>());
+    return run(Tall<320>());
 }
 
 }  // namespace svdq

@@ -109,7 +109,9 @@ SHAPES = [(1, 8, 64), (1, 4096, 128), (1, 264, 4096), (2, 64, 192), (15, 72, 320
           (17, 200, 448), (33, 328, 1024), (64, 64, 576), (65, 1032, 192), (127, 520, 704),
           (128, 2048, 256), (129, 136, 2048), (255, 1000, 64), (257, 4104, 128), (300, 300 * 8, 320),
           (1000, 1000, 1088), (2048, 2048, 512), (2049, 2056, 192), (4000, 4104, 320),
-          (4097, 4352, 128), (5, 24, 131072)]
+          (4097, 4352, 128), (5, 24, 131072), (64, 8192, 320), (61, 8184, 64), (120, 8200, 1216),
+          (630, 4096, 192), (601, 4104, 704), (1000, 4096, 448), (2040, 4096, 320), (2990, 4096, 192),
+          (4096, 4096, 256), (4601, 4096, 512), (4608, 4088, 64), (7, 1000, 448), (3, 40, 576)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
