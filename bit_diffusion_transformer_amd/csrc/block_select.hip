@@ -93,6 +93,22 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 
 constexpr int kChooseWaves = 8;
 
+// x OR-ed over the wave, every lane getting it: lane exchanges within 16 lanes,
+// then the swaps with the lanes 16 and 32 away.
+__device__ __forceinline__ uint32_t wave_or(uint32_t x) {
+    x |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true);    // lane ^ 1
+    x |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true);    // lane ^ 2
+    x |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true);   // 7 - lane
+    x |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true);   // 15 - lane
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = a[0] | a[1];
+    const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return b[0] | b[1];
+}
+__device__ __forceinline__ uint64_t wave_or64(uint64_t x) {
+    return (uint64_t)wave_or((uint32_t)(x >> 32)) << 32 | wave_or((uint32_t)x);
+}
+
 // The `keep` highest of a query block's keys, by one wave: the largest
 // threshold that at least `keep` keys reach, bit by bit below the first bit in
 // which the highest and the lowest key differ (one ballot per 64 keys and bit,
@@ -120,16 +136,13 @@ __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, in
     uint64_t at = 1;                                         // keys >= at are taken,
     int ties = 0x7FFFFFFF;                                   // `ties` of those equal to it at most
     if (valid > keep) {
-        uint64_t any = 0, all = ~0ull;                       // bits set in some / in every valid key
+        uint64_t any = 0, none = 0;                          // bits set / clear in some valid key
         each([&](uint64_t y, int) {
             any |= y;
-            all &= y ? y : ~0ull;
+            none |= y ? ~y : 0;
         });
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-            any |= __shfl_xor(any, d);
-            all &= __shfl_xor(all, d);
-        }
+        any = wave_or64(any);
+        const uint64_t all = ~wave_or64(none);
         const uint64_t differ = any & ~all;
         int bit = differ ? 63 - __builtin_clzll(differ) : -1;
         at = bit < 0 ? all : bit == 63 ? 0 : all & ~((2ull << bit) - 1);
@@ -193,15 +206,15 @@ block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
     const int valid = (int)((valid_keys(kv_len, b, a.seq_k) + kKB - 1) / kKB);
     const int c = lane & 15, g = lane >> 4;
     // Blocks past the end, or without a valid key, have no mean: what is read in
-    // their place is another one of the tile or what the workspace held, and is
-    // used for no key.
+    // their place is what the workspace held, and is used for no key.  (The loads
+    // do not wait for the length.)
     const f64x2 *kp = km + kplane * mean_tiles(a.nk) * (8 * D) + lane;
     f64x2 qf[STEPS], kf[STEPS];
     auto load_k = [&](int j0) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) kf[s] = kp[(int64_t)(j0 >> 4) * (8 * D) + 64 * s];
     };
-    if (16 * wave < valid) load_k(16 * wave);
+    if (16 * wave < nk) load_k(16 * wave);
     {
         const int64_t i = i0 + (c < R ? c : R - 1);
         const f64x2 *p = qm + plane * mean_tiles(a.nq) * (8 * D) +
@@ -211,15 +224,14 @@ block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
     }
     for (int j0 = 16 * wave; j0 < nk; j0 += 16 * kChooseWaves) {
         const int j = j0 + c;
-        f64x4 acc = {};
-        if (j0 < valid) {                                    // uniform
+        f64x4 acc = {}, odd = {};                            // two chains of products
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].x, kf[s].x, acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].y, kf[s].y, acc, 0, 0, 0);
-            }
-            if (j0 + 16 * kChooseWaves < valid) load_k(j0 + 16 * kChooseWaves);
+        for (int s = 0; s < STEPS; ++s) {
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].x, kf[s].x, acc, 0, 0, 0);
+            odd = __builtin_amdgcn_mfma_f64_16x16x4f64(qf[s].y, kf[s].y, odd, 0, 0, 0);
         }
+        acc += odd;
+        if (j0 + 16 * kChooseWaves < nk) load_k(j0 + 16 * kChooseWaves);
         if (j < nk)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
