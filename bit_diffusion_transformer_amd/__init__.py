@@ -37,7 +37,7 @@ from ._attention import (EXPORTS_ATTENTION, AttentionShape, KEY_BLOCK, QUERY_BLO
                          svdq_block_attention_workspace_bytes, svdq_qkv_norm_rope,
                          svdq_rope_tables, svdq_select_blocks, svdq_select_blocks_workspace_bytes,
                          svdq_sparse_attention, svdq_sparse_attention_workspace_bytes)
-from ._int8 import (EXPORTS_I8, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
+from ._int8 import (EXPORTS_I8, I8Linear, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
                     i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,
                     svdq_i8_linear_workspace_bytes, svdq_i8_pack_weights, svdq_i8_quantize_act)
 

@@ -88,13 +88,23 @@ def svdq_sparse_attention(q, k, v, kv_len, shape: AttentionShape, scale, blocks,
 
 # ------------------------------------------------------------- tensor level
 
+def _int32(n, what: str) -> int:
+    """n as a C int32 (ctypes would drop higher bits silently)."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError("%s: %d is out of range" % (what, n))
+    return n
+
+
 def rope_axes(dims: Sequence[int], theta=10000.0) -> RopeAxes:
     """How a head's dimension is divided among the axes; theta: one number, or one per axis."""
-    dims = [int(d) for d in dims]
+    dims = [_int32(d, "dims") for d in dims]
     if not 1 <= len(dims) <= ROPE_MAX_AXES:
         raise ValueError("1 to %d axes, got %d" % (ROPE_MAX_AXES, len(dims)))
-    thetas = [float(theta)] * len(dims) if isinstance(theta, (int, float)) else \
-        [float(t) for t in theta]
+    try:
+        thetas = [float(theta)] * len(dims)
+    except TypeError:
+        thetas = [float(t) for t in theta]
     if len(thetas) != len(dims):
         raise ValueError("%d dims and %d thetas" % (len(dims), len(thetas)))
     a = RopeAxes(axes=len(dims))
@@ -145,7 +155,7 @@ def _shape(q, k, kv_len, keep, first) -> AttentionShape:
     _, G, Sk, _ = expect(k, "k", BF16, (B, None, None, D))
     if kv_len is not None:
         expect(kv_len, "kv_len", I32, (B,))
-    return AttentionShape(B, Sq, Sk, H, G, D, keep, first)
+    return AttentionShape(B, Sq, Sk, H, G, D, _int32(keep, "keep"), _int32(first, "first"))
 
 
 def _lists(s: AttentionShape):

@@ -115,3 +115,29 @@ def i8_linear(X, lam, qw, sw, bias=None, act: int = ACT_NONE,
     with on(dev):
         svdq_i8_linear(X, lam, qw, sw, bias, act, M, N, K, Y, ws, need)
     return Y
+
+
+class I8Linear:
+    """An 8-bit replacement for one linear layer, beside SVDQLinear for the layers that lose
+    too much in 4 bits: ``from_weight`` packs the weight (and the smoothing factors' inverse
+    into it) on the GPU once, ``__call__`` runs the layer."""
+
+    def __init__(self, lam, qw, sw, bias=None, act: int = ACT_NONE):
+        self.lam, self.qw, self.sw, self.bias, self.act = lam, qw, sw, bias, act
+
+    @classmethod
+    def from_weight(cls, W, lam=None, bias=None, act: int = ACT_NONE):
+        """W fp32 [N, K] of Y = X W^T; lam fp32 [K] smooths the activations (X / lam, W lam)."""
+        qw, sw = i8_pack_weights(W if lam is None else W * lam)
+        return cls(lam, qw, sw, bias, act)
+
+    @property
+    def in_features(self) -> int:
+        return self.qw.shape[1]
+
+    @property
+    def out_features(self) -> int:
+        return self.qw.shape[0]
+
+    def __call__(self, X: torch.Tensor) -> torch.Tensor:
+        return i8_linear(X, self.lam, self.qw, self.sw, self.bias, self.act)

@@ -136,6 +136,11 @@ def test_tensor_functions_refuse_bad_tensors():
         bdt.rope_tables(pos, (16, 56, 56), theta=(1e4, 1e4))
     with pytest.raises(ValueError):
         bdt.rope_tables(torch.zeros(4, 5), (16,) * 5)
+    with pytest.raises(ValueError, match="range"):
+        bdt.rope_axes((2 ** 32 + 16,))
+    with pytest.raises(ValueError, match="range"):
+        bdt.select_blocks(torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16),
+                          torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16), 2 ** 32 + 1)
     qkv = torch.zeros(8, 3 * 2 * 64, dtype=torch.bfloat16)
     t = torch.zeros(4, 32)
     with pytest.raises(ValueError, match="GPU"):

@@ -197,6 +197,19 @@ def test_linear_is_its_two_steps(M, N, K, smooth, act):
     assert bool(((Y.double() - full).abs() <= 1.13 * step * 1.001 + 2.0 ** -8 * full.abs() + 1e-6).all())
 
 
+def test_layer_object_is_the_linear():
+    g = torch.Generator(device=DEV).manual_seed(6)
+    W, lam = torch.randn(72, 320, generator=g, device=DEV), 0.5 + torch.rand(320, generator=g, device=DEV)
+    bias = torch.randn(72, generator=g, device=DEV).to(torch.bfloat16)
+    X = torch.randn(9, 320, generator=g, device=DEV).to(torch.bfloat16)
+    layer = bdt.I8Linear.from_weight(W, lam, bias, bdt.ACT_GELU)
+    assert (layer.in_features, layer.out_features) == (320, 72)
+    qw, sw = bdt.i8_pack_weights(W * lam)
+    assert torch.equal(layer(X), bdt.i8_linear(X, lam, qw, sw, bias, bdt.ACT_GELU))
+    plain = bdt.I8Linear.from_weight(W)
+    assert torch.equal(plain(X), bdt.i8_linear(X, None, *bdt.i8_pack_weights(W)))
+
+
 @pytest.mark.parametrize("M", [1, 100, 1100])
 def test_linear_in_a_graph_and_on_two_streams(M):
     K, N = 1024, 1536
