@@ -29,58 +29,6 @@ __device__ __forceinline__ int64_t mean_at(int64_t blk, int p) {
 }
 __host__ __device__ inline int64_t mean_tiles(int64_t blocks) { return (blocks + 15) / 16; }
 
-// Means over blocks of rows.  One workgroup per block of one head: 16-byte
-// loads, 16 (D = 128) or 32 (D = 64) rows at a time, 64-bit sums of eight
-// columns a thread, then a sum over the rows through LDS.  Bound by reading Q
-// and K once.  Stored in the order in which the score kernel's matrix
-// instruction takes them (mean_at), so that each of its loads is one run.
-template <int D>
-__global__ void __launch_bounds__(256)
-block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
-                   const int32_t *__restrict__ kv_len, AttnShape a, f64x2 *__restrict__ qm,
-                   f64x2 *__restrict__ km) {
-    constexpr int LANES = D / 8, ROWS = 256 / LANES;
-    __shared__ double part[ROWS / 2][D];
-    // neighbouring blocks' means share cache lines: one XCD writes them
-    const int64_t wg = xcd_range(blockIdx.x, a.planes_q * a.nq + a.planes_k * a.nk);
-    const bool query = wg < a.planes_q * a.nq;               // uniform
-    const int64_t id = query ? wg : wg - a.planes_q * a.nq;
-    const int64_t nb = query ? a.nq : a.nk, size = query ? kQB : kKB;
-    const int64_t plane = id / nb, blk = id - plane * nb;
-    const int64_t seq = query ? a.seq_q : a.seq_k;
-    const int64_t have = query ? a.seq_q : valid_keys(kv_len, plane / a.G, a.seq_k);
-    const int64_t left = have - blk * size;
-    const int rows = (int)(left < size ? left : size);
-    if (rows <= 0) return;                                   // a key block without a valid key
-    const uint16_t *src = (query ? q : k) + (plane * seq + blk * size) * D;
-    const int r0 = threadIdx.x / LANES, c = threadIdx.x % LANES;
-    double s[8] = {};
-    for (int r = r0; r < rows; r += ROWS) {
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(src + r * D + 8 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[2 * i] += (double)bf16_lo(x[i]);
-            s[2 * i + 1] += (double)bf16_hi(x[i]);
-        }
-    }
-    for (int half = ROWS / 2; half >= 1; half >>= 1) {
-        if (r0 >= half && r0 < 2 * half)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) part[r0 - half][8 * c + i] = s[i];
-        __syncthreads();
-        if (r0 < half)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += part[r0][8 * c + i];
-        __syncthreads();
-    }
-    if (r0 == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            (query ? qm : km)[plane * mean_tiles(nb) * (8 * D) + mean_at<D>(blk, 4 * c + i)] =
-                f64x2{s[2 * i] / rows, s[2 * i + 1] / rows};
-    }
-}
-
 // A score as an unsigned key in the same order (-0 as +0), at least 1; a NaN
 // counts as the lowest.  Key 0: a block that must not be taken.
 __device__ __forceinline__ uint64_t order_key(double x) {
@@ -89,6 +37,104 @@ __device__ __forceinline__ uint64_t order_key(double x) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
     const uint64_t o = u >> 63 ? ~u : u | 0x8000000000000000ull;
     return o ? o : 1;
+}
+
+// One query block of few rows: the workgroup of a key block sums them itself, in
+// its 16 groups of threads (one head each at a time), and stores the block's
+// scores instead of its means.  Selection over 20000 keys for 2 x 16 heads (4 of
+// keys), by scores | by means: 1 row 18.4 | 23.2 us, 16 rows 21.1 | 23.3 us; 64
+// rows of 24 heads (24 of keys) 67 | 38 us.
+__host__ __device__ inline bool few_queries(const AttnShape &a) {
+    return a.nq == 1 && a.nk > 0 && a.seq_q * ((a.H / a.G + 15) / 16) <= 16;
+}
+
+// Means over blocks of rows.  One workgroup per block of one head: 16-byte
+// loads, 64 rows' at once, 64-bit sums of eight columns a thread, then sums over
+// the threads of a wave and, through LDS, over the waves.  Bound by reading Q and
+// K once.  Stored in the order in which the score kernel's matrix
+// instruction takes them (mean_at), so that each of its loads is one run.
+//
+// FEW: one query block of few rows (few_queries).  Workgroups for key blocks
+// only; LANES threads a query head then sum its rows, and the block's scores go
+// out instead of its means.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(256)
+block_means_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
+                   const int32_t *__restrict__ kv_len, AttnShape a, f64x2 *__restrict__ qm,
+                   f64x2 *__restrict__ km, uint64_t *__restrict__ scores) {
+    constexpr int LANES = D / 8, ROWS = 256 / LANES;   // rows at a time
+    __shared__ double part[4][D];
+    const int64_t query_wgs = FEW ? 0 : a.planes_q * a.nq;
+    // neighbouring blocks' means share cache lines: one XCD writes them
+    const int64_t wg = xcd_range(blockIdx.x, query_wgs + a.planes_k * a.nk);
+    const bool query = wg < query_wgs;                       // uniform
+    const int64_t id = query ? wg : wg - query_wgs;
+    const int64_t nb = query ? a.nq : a.nk, size = query ? kQB : kKB;
+    const int64_t plane = id / nb, blk = id - plane * nb;
+    const int64_t seq = query ? a.seq_q : a.seq_k;
+    const int64_t have = query ? a.seq_q : valid_keys(kv_len, plane / a.G, a.seq_k);
+    const int64_t left = have - blk * size;
+    const int rows = (int)(left < size ? left : size);
+    if (rows <= 0) return;                                   // a key block without a valid key
+    const int r0 = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    auto add = [](double *s, const u32x4 x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[2 * i] += (double)bf16_lo(x[i]);
+            s[2 * i + 1] += (double)bf16_hi(x[i]);
+        }
+    };
+    auto row_of = [&](const uint16_t *src, int r) {
+        return *reinterpret_cast<const u32x4 *>(src + r * D + 8 * c);
+    };
+    const int group = a.H / a.G;
+    const int64_t head0 = plane / a.G * a.H + plane % a.G * group;   // the first that reads these keys
+    u32x4 first = {};                                        // row 0 of the group's first head
+    if (FEW && r0 < group) first = row_of(q + (head0 + r0) * a.seq_q * D, 0);
+    const uint16_t *src = (query ? q : k) + (plane * seq + blk * size) * D;
+    double s[8] = {};
+    for (int r = r0; r < rows; r += kKB) {                   // 64 rows' loads at once
+        u32x4 x[kKB / ROWS];
+#pragma unroll
+        for (int i = 0; i < kKB / ROWS; ++i)
+            x[i] = row_of(src, r + i * ROWS < rows ? r + i * ROWS : rows - 1);
+#pragma unroll
+        for (int i = 0; i < kKB / ROWS; ++i) add(s, r + i * ROWS < rows ? x[i] : u32x4{});
+    }
+    // over the rows of a wave (lanes LANES, 2 LANES .. apart), then over the waves
+#pragma unroll
+    for (int m = LANES; m < 64; m <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += __shfl_xor(s[i], m);
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) < LANES)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wave][8 * c + i] = s[i];
+    __syncthreads();
+    double mean[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        mean[i] = (part[0][8 * c + i] + part[1][8 * c + i] + part[2][8 * c + i] +
+                   part[3][8 * c + i]) / rows;
+    if (!FEW) {
+        if (r0 == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                (query ? qm : km)[plane * mean_tiles(nb) * (8 * D) + mean_at<D>(blk, 4 * c + i)] =
+                    f64x2{mean[2 * i], mean[2 * i + 1]};
+        return;
+    }
+    for (int h = r0; h < group; h += ROWS) {
+        const uint16_t *qh = q + (head0 + h) * a.seq_q * D;
+        double t[8] = {}, dot = 0;
+        add(t, h == r0 ? first : row_of(qh, 0));
+        for (int r = 1; r < a.seq_q; ++r) add(t, row_of(qh, r));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot += t[i] / (double)a.seq_q * mean[i];
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) dot += __shfl_xor(dot, m);
+        if (c == 0) scores[(head0 + h) * a.nk + blk] = order_key(dot);
+    }
 }
 
 constexpr int kChooseWaves = 8;
@@ -250,6 +296,26 @@ block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
     }
 }
 
+// The same choice from stored scores: one workgroup per head (few_queries).
+__global__ void __launch_bounds__(256)
+block_choose_few_kernel(const uint64_t *__restrict__ scores, const int32_t *__restrict__ kv_len,
+                        AttnShape a, int32_t *__restrict__ blocks) {
+    extern __shared__ uint64_t keys[];                       // [nk]
+    const int64_t plane = blockIdx.x;
+    const int nk = (int)a.nk;
+    const int valid = (int)((valid_keys(kv_len, plane / a.H, a.seq_k) + kKB - 1) / kKB);
+    for (int j = threadIdx.x; j < nk; j += 256) {
+        const uint64_t x = scores[plane * nk + j];
+        keys[j] = j >= valid ? 0ull : j < a.first ? ~0ull : x;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    int32_t *out = blocks + plane * a.keep;
+    if (nk <= 128) choose<2>(keys, nk, valid, a.keep, threadIdx.x, out);
+    else if (nk <= 512) choose<8>(keys, nk, valid, a.keep, threadIdx.x, out);
+    else choose<0>(keys, nk, valid, a.keep, threadIdx.x, out);
+}
+
 namespace {
 
 // 64-bit means of a side, its blocks in tiles of 16.
@@ -269,10 +335,20 @@ int choose_rows(const AttnShape &a) {
 template <int D>
 hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, const AttnShape &a,
                   int32_t *blocks, void *ws, hipStream_t stream) {
+    if (few_queries(a)) {
+        uint64_t *scores = static_cast<uint64_t *>(ws);
+        block_means_kernel<D, true><<<(unsigned)(a.planes_k * a.nk), 256, 0, stream>>>(
+            q, k, kv_len, a, nullptr, nullptr, scores);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        block_choose_few_kernel<<<(unsigned)a.planes_q, 256, (size_t)a.nk * 8, stream>>>(
+            scores, kv_len, a, blocks);
+        return hipGetLastError();
+    }
     f64x2 *qm = static_cast<f64x2 *>(ws);
     f64x2 *km = reinterpret_cast<f64x2 *>(static_cast<char *>(ws) + means_bytes(a.planes_q, a.nq, D));
-    block_means_kernel<D><<<(unsigned)(a.planes_q * a.nq + a.planes_k * a.nk), 256, 0, stream>>>(
-        q, k, kv_len, a, qm, km);
+    block_means_kernel<D, false><<<(unsigned)(a.planes_q * a.nq + a.planes_k * a.nk), 256, 0, stream>>>(
+        q, k, kv_len, a, qm, km, nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int R = choose_rows(a);
@@ -285,6 +361,7 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, c
 }  // namespace
 
 size_t select_workspace(const AttnShape &a) {
+    if (few_queries(a)) return align256((size_t)a.planes_q * (size_t)a.nk * 8);
     return means_bytes(a.planes_q, a.nq, a.D) + means_bytes(a.planes_k, a.nk, a.D);
 }
 
