@@ -199,6 +199,31 @@ def test_given_lists_are_read_by_the_documented_rule(D, Sq):
     assert bool((out[1, :QB] == 0).all())
 
 
+@pytest.mark.parametrize("H,G,D,Sq,Sk,keep", [
+    (40, 1, 128, 3, 700, 5),           # more heads per K head than a workgroup has groups of threads
+    (35, 1, 64, 1, 1300, 9),
+    (6, 2, 128, 16, 2000, 7), (6, 2, 128, 17, 2000, 7),
+    (17, 1, 64, 8, 900, 4), (17, 1, 64, 9, 900, 4),
+    (2, 2, 64, 127, 320, 2), (2, 2, 64, 1, 64, 1),
+])
+def test_few_queries(H, G, D, Sq, Sk, keep):
+    """One query block, from one row to nearly all of it; a sequence that ends inside a key
+    block and one without keys."""
+    kv = [Sk - 1, 0, Sk]
+    q, k, v = inputs(3, H, G, D, Sq, Sk, Sq + H)
+    kv_len = torch.tensor(kv, dtype=torch.int32, device=DEV)
+    k[0, :, Sk - 1] = float("nan")
+    out, blocks = bdt.sparse_attention(q, k, v, keep, first=1, kv_len=kv_len, return_blocks=True)
+    want = lists_64(q, k, kv, keep, 1)
+    assert torch.equal(blocks.cpu(), want)
+    ref, tol = attention_64(q, k, v, want, D ** -0.5, kv)
+    check(out, ref, tol, "few queries")
+    ones, kind = torch.ones_like(q), torch.arange(Sk, device=DEV) // KB % 2      # many ties
+    alike = kind.to(torch.bfloat16)[None, None, :, None].expand_as(k).contiguous()
+    same = bdt.select_blocks(ones, alike, keep)
+    assert torch.equal(same.cpu(), lists_64(ones, alike, None, keep, 0))
+
+
 @pytest.mark.parametrize("gain", [0.0, 40.0, 4000.0])
 @pytest.mark.parametrize("Sq", [2, 400])
 def test_extreme_scores(gain, Sq):
