@@ -12,6 +12,15 @@
 // memory straight into LDS (two buffers, the next block's copies in flight
 // while the current one is used); K is read in 16-byte pieces, V through the
 // transposing 8-byte LDS read.
+//
+// 12 heads of 32760 queries, 64 of 512 blocks each, D = 128: 800-840 us, about 1
+// PFLOP/s; 48 heads of 4608, 24 of 72 blocks: 195-208 us; 24 heads of 16384, 32
+// of 256 blocks, D = 64: 262 us.  The matrix units are busy half the time, and the
+// parts add up: the two products and their LDS reads alone take 609 us where the whole takes 800
+// (at the 1.7 GHz that their power leaves), the softmax 111 more, the copies (32
+// KB per 128 x 64 scores) the rest.  Two waves share a SIMD; a wave's key block
+// costs it 790 cycles to issue copies, 770 for S, 1190 for the softmax, 1130 for
+// the second product and 130 at the barrier.
 #include "attention_internal.h"
 #include "svdq_wave.h"
 
@@ -66,7 +75,9 @@ struct Lds {
     uint8_t k[2][TILE];
     uint8_t v[2][TILE];
     uint16_t list[kMaxList];
-    int count;
+    // The list's length, until the first copies into this buffer (after the first
+    // key block's barrier): at D = 64 four workgroups' LDS are 160 KB exactly.
+    __device__ int *count() { return reinterpret_cast<int *>(v[1]); }
 };
 
 // The list's usable entries, in order: not negative, below `valid`, above every
@@ -95,8 +106,10 @@ __device__ __forceinline__ void read_list(const int32_t *__restrict__ blocks, in
     if (lane == 0) *count = n;
 }
 
+// Two workgroups per compute unit at D = 128 (LDS and registers); four at D = 64
+// (24 heads of 16384, 32 blocks each: 262 us, three take 270).
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, D == 64 ? 4 : 2)
 block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
                        const uint16_t *__restrict__ v, const int32_t *__restrict__ kv_len,
                        AttnShape a, float scale_log2, const int32_t *__restrict__ blocks,
@@ -123,9 +136,9 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
         len = n < 0 ? 0 : n > len ? len : n;
     }
     if (wave == 0)
-        read_list(blocks + id * a.keep, a.keep, (len + kKB - 1) / kKB, lds.list, &lds.count);
+        read_list(blocks + id * a.keep, a.keep, (len + kKB - 1) / kKB, lds.list, lds.count());
     __syncthreads();
-    int first = 0, last = lds.count;
+    int first = 0, last = *lds.count();
     if (SPLIT) {
         const int n = last;
         first = (int)((int64_t)n * piece / splits);
@@ -342,7 +355,7 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
 // Joins the pieces of each row: the largest maximum, weights 2^(m_i - m) on sums
 // and results.  D / 4 lanes per row, whose first lanes hold one piece's maximum
 // and sum each (D / 4 >= 16 pieces at a time), so that the loads of all pieces
-// are in flight together.
+// are in flight together.  32 rows of 8 pieces: 4.6 us, 3 of them the launch.
 template <int D>
 __global__ void __launch_bounds__(256)
 join_kernel(const float *__restrict__ part, const float *__restrict__ stat, AttnShape a, int splits,

@@ -53,6 +53,7 @@ __host__ __device__ inline bool few_queries(const AttnShape &a) {
 // the threads of a wave and, through LDS, over the waves.  Bound by reading Q and
 // K once.  Stored in the order in which the score kernel's matrix
 // instruction takes them (mean_at), so that each of its loads is one run.
+// 12 heads of 32760 x 128, Q and K: 38 us, 5.3 TB/s.
 //
 // FEW: one query block of few rows (few_queries).  Workgroups for key blocks
 // only; LANES threads a query head then sum its rows, and the block's scores go
@@ -234,6 +235,9 @@ __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, in
 // registers throughout, tiles of key blocks shared among the waves; the order
 // of k is free, so a lane takes two neighbouring columns in one 16-byte load.
 // The keys go to LDS, where a wave then chooses for each of its query blocks.
+// 12 heads of 256 x 512 blocks: 24.8 us, of which the choice takes 10 (about 18
+// bits, eight ballots each), the products 5 and their loads 5; 48 heads of 36 x
+// 72 blocks: 9.8 us.
 template <int D>
 __global__ void __launch_bounds__(64 * kChooseWaves)
 block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
@@ -296,7 +300,8 @@ block_choose_kernel(const f64x2 *__restrict__ qm, const f64x2 *__restrict__ km,
     }
 }
 
-// The same choice from stored scores: one workgroup per head (few_queries).
+// The same choice from stored scores: one workgroup per head (few_queries).  32
+// heads of 313 blocks: 5.8 us, about 3 of them the launch and the loads.
 __global__ void __launch_bounds__(256)
 block_choose_few_kernel(const uint64_t *__restrict__ scores, const int32_t *__restrict__ kv_len,
                         AttnShape a, int32_t *__restrict__ blocks) {

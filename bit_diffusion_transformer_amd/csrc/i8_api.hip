@@ -37,11 +37,10 @@ int32_t check_workspace(const void *ws, size_t ws_bytes, size_t need) {
 struct Workspace {
     int8_t *qa;
     float *sa;
-    void *gemm;
     size_t bytes;
 };
 
-Workspace carve(void *base, int64_t M, int64_t N, int64_t K) {
+Workspace carve(void *base, int64_t M, int64_t K) {
     char *p = static_cast<char *>(base);
     Workspace w{};
     size_t off = 0;
@@ -49,8 +48,6 @@ Workspace carve(void *base, int64_t M, int64_t N, int64_t K) {
     off += align256((size_t)M * (size_t)K);
     w.sa = reinterpret_cast<float *>(p + off);
     off += align256((size_t)M * 4);
-    w.gemm = p + off;
-    off += i8_gemm_workspace(M, N, K);
     w.bytes = off;
     return w;
 }
@@ -91,8 +88,8 @@ int32_t svdq_i8_quantize_act(const uint16_t *X, const float *lambda, int64_t M, 
 }
 
 size_t svdq_i8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M < 0 || N < 0 || K < 0) return 0;
-    return i8_gemm_workspace(M, N, K);
+    (void)M, (void)N, (void)K;
+    return 0;
 }
 
 int32_t svdq_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
@@ -107,16 +104,15 @@ int32_t svdq_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const 
     SVDQ_TRY(need_ptr(sw, "sw"));
     SVDQ_TRY(need_ptr(Y, "Y"));
     if (bias) SVDQ_TRY(need_ptr(bias, "bias"));
-    SVDQ_TRY(check_workspace(workspace, ws_bytes, i8_gemm_workspace(M, N, K)));
     SVDQ_TRY(check_device());
-    return hip_status(launch_i8_gemm(qa, sa, qw, sw, bias, act, M, N, K, Y, workspace,
-                                     (hipStream_t)stream),
+    (void)workspace, (void)ws_bytes;
+    return hip_status(launch_i8_gemm(qa, sa, qw, sw, bias, act, M, N, K, Y, (hipStream_t)stream),
                       "i8_gemm launch");
 }
 
 size_t svdq_i8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0) return 0;
-    return carve(nullptr, M, N, K).bytes;
+    return carve(nullptr, M, K).bytes;
 }
 
 int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw, const float *sw,
@@ -131,13 +127,13 @@ int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw,
     SVDQ_TRY(need_ptr(sw, "sw"));
     SVDQ_TRY(need_ptr(Y, "Y"));
     if (bias) SVDQ_TRY(need_ptr(bias, "bias"));
-    SVDQ_TRY(check_workspace(workspace, ws_bytes, carve(nullptr, M, N, K).bytes));
+    SVDQ_TRY(check_workspace(workspace, ws_bytes, carve(nullptr, M, K).bytes));
     SVDQ_TRY(check_device());
-    const Workspace w = carve(workspace, M, N, K);
+    const Workspace w = carve(workspace, M, K);
     hipStream_t s = (hipStream_t)stream;
     SVDQ_TRY(hip_status(launch_i8_quantize(X, false, lambda, M, K, w.qa, w.sa, s),
                         "i8_quantize_act launch"));
-    return hip_status(launch_i8_gemm(w.qa, w.sa, qw, sw, bias, act, M, N, K, Y, w.gemm, s),
+    return hip_status(launch_i8_gemm(w.qa, w.sa, qw, sw, bias, act, M, N, K, Y, s),
                       "i8_gemm launch");
 }
 

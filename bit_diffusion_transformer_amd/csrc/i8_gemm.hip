@@ -10,6 +10,14 @@
 // conflicts), and the integer sums stay in registers over the whole K loop
 // (exact: K <= 2^17).  The epilogue scales in fp32, adds the bias, applies
 // the activation and rounds once.
+//
+// Measured with inputs that change from call to call (operations: two per code
+// product).  4096 x 4096 -> 16384 with GELU: 263 us, 2.09 POP/s; 4608 x 12288 ->
+// 4096: 215 us, 2.16 POP/s: the matrix units' issue at the clock that their power
+// leaves.  One token, 4096 -> 24576: 18.8 us, 5.4 TB/s of weights.  333 tokens,
+// 4096 -> 4096: 15 us, of which 4 are a launch with one stage; every further
+// stage of 128 costs 0.35 us (two workgroups' barrier, 32 KB of copies, 64 KB of
+// fragment reads), whether its operands are in the L2s or not.
 #include "i8_internal.h"
 #include "svdq_wave.h"
 
@@ -301,12 +309,10 @@ int64_t tiles(int64_t M, int64_t N) {
 using namespace i8;
 
 int64_t i8_gemm_groups(int64_t M, int64_t N) { return tiles<Small>(M, N); }
-size_t i8_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
                           const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,
-                          uint16_t *Y, void *workspace, hipStream_t stream) {
-    (void)workspace;
+                          uint16_t *Y, hipStream_t stream) {
     const int64_t cus = wg_slots() / 2;
     auto run = [&](auto t) {
         typedef decltype(t) T;

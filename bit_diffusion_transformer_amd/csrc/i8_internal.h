@@ -15,8 +15,7 @@ int64_t i8_quantize_groups(int64_t M);   // workgroups at most, of 512
 
 hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
                           const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,
-                          uint16_t *Y, void *workspace, hipStream_t stream);
+                          uint16_t *Y, hipStream_t stream);
 int64_t i8_gemm_groups(int64_t M, int64_t N);       // workgroups at most, of 512
-size_t i8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 
 }  // namespace svdq

@@ -11,7 +11,9 @@
  * work enqueued on `stream` without synchronizing; every argument checked
  * before anything is launched, arguments first, then the device; buffers
  * owned by the caller, nothing allocated, no state kept; outputs must not
- * alias inputs; results deterministic (no atomics).
+ * alias inputs; results deterministic (no atomics).  A workspace serves one
+ * call at a time: calls that may run at once (on two streams, in two captured
+ * graphs) need one each.
  */
 #ifndef SVDQ_ATTENTION_H
 #define SVDQ_ATTENTION_H
@@ -87,7 +89,7 @@ typedef struct svdq_attention_shape {
     int32_t first;      /* 0 .. keep: the first `first` key blocks are always taken (and count) */
 } svdq_attention_shape;
 
-/* Workspace of svdq_select_blocks: the blocks' means. */
+/* Workspace of svdq_select_blocks: the blocks' means, or their scores. */
 size_t svdq_select_blocks_workspace_bytes(const svdq_attention_shape *shape);
 
 /*

@@ -12,7 +12,8 @@
  * svdq_quantize_act_down).  The products are summed exactly in 32-bit
  * integers (K <= SVDQ_I8_MAX_K keeps every sum below 2^31).
  *
- * Conventions and status codes are those of svdq.h.
+ * Conventions and status codes are those of svdq.h.  A workspace serves one
+ * call at a time.
  */
 #ifndef SVDQ_I8_H
 #define SVDQ_I8_H
@@ -48,8 +49,8 @@ int32_t svdq_i8_pack_weights(const float *W, int64_t N, int64_t K, int8_t *qw, f
 int32_t svdq_i8_quantize_act(const uint16_t *X, const float *lambda, int64_t M, int64_t K,
                              int8_t *qa, float *sa, void *stream);
 
-/* Workspace of svdq_i8_gemm: integer partial sums where few output tiles are
- * split over K (0 elsewhere). */
+/* Workspace of svdq_i8_gemm.  No shape needs any: 0, and `workspace` may be
+ * NULL. */
 size_t svdq_i8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
