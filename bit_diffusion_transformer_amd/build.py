@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsvdq.so")
 SOURCES = ["svdq_api.hip", "quant_down.hip", "w4a4_gemm.hip", "w4a4_gemm_qkv.hip", "w4a4_gemm_mlp.hip",
            "w4a4_mx_gemm.hip", "awq_w4a16.hip", "w4a4_gemm_sums.hip", "w4a4_gemm_ks.hip",
-           "attention_api.hip", "qkv_rope.hip", "block_select.hip", "block_attention.hip", "i8_api.hip", "i8_quantize.hip", "i8_gemm.hip"]
+           "attention_api.hip", "qkv_rope.hip", "block_select.hip", "block_attention.hip",
+           "i8_api.hip", "i8_quantize.hip", "i8_gemm.hip", "i8_few.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

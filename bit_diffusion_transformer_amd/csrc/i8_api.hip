@@ -129,8 +129,11 @@ int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw,
     if (bias) SVDQ_TRY(need_ptr(bias, "bias"));
     SVDQ_TRY(check_workspace(workspace, ws_bytes, carve(nullptr, M, K).bytes));
     SVDQ_TRY(check_device());
-    const Workspace w = carve(workspace, M, K);
     hipStream_t s = (hipStream_t)stream;
+    if (i8_few_tokens(M, N, K))
+        return hip_status(launch_i8_few(X, lambda, qw, sw, bias, act, M, N, K, Y, s),
+                          "i8_linear launch");
+    const Workspace w = carve(workspace, M, K);
     SVDQ_TRY(hip_status(launch_i8_quantize(X, false, lambda, M, K, w.qa, w.sa, s),
                         "i8_quantize_act launch"));
     return hip_status(launch_i8_gemm(w.qa, w.sa, qw, sw, bias, act, M, N, K, Y, s),

@@ -18,6 +18,7 @@
 // 4096 -> 4096: 15 us, of which 4 are a launch with one stage; every further
 // stage of 128 costs 0.35 us (two workgroups' barrier, 32 KB of copies, 64 KB of
 // fragment reads), whether its operands are in the L2s or not.
+#include "i8_device.h"
 #include "i8_internal.h"
 #include "svdq_wave.h"
 
@@ -27,22 +28,7 @@ namespace svdq {
 
 namespace i8 {
 
-constexpr int kRow = 128;        // bytes of a row per stage
 constexpr int kGroupM = 8;       // m tiles per raster group (L2 reuse of weights)
-
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-// 32x32 output tile, K = 32 int8 per call: lane l supplies 16 bytes of row /
-// column l % 32, k half l / 32; output element i of lane l is row
-// 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32.
-__device__ __forceinline__ i32x16 mfma_i8_32x32x32(i32x4 a, i32x4 b, i32x16 c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
-}
-
-// The 16-byte segment s of a row sits at slot s ^ swz(row): any 8 consecutive
-// rows of one segment touch 8 distinct slots (all banks of a 128-byte pass),
-// any 16 consecutive rows 16 distinct 16-byte groups of 256 bytes.
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // WM x WN waves cover a tile; KS such groups share its stages of K in turn (stage
 // s goes to group s % KS), each with a ring of its own, and add their sums at

@@ -1,74 +1,13 @@
 // i8_quantize.hip -- 8-bit row quantization: the activations' step (with
 // optional smoothing) and the offline packing of the weights.
+#include "i8_device.h"
 #include "i8_internal.h"
-#include "svdq_device.h"
 
 namespace svdq {
 
+using namespace i8;
+
 namespace {
-
-// Eight consecutive values of a row as they are loaded (16 bytes of bf16, 32 of
-// fp32), and as fp32.
-template <bool F32>
-struct Raw {
-    u32x4 w[F32 ? 2 : 1];
-};
-
-template <bool F32>
-__device__ __forceinline__ Raw<F32> load_raw(const void *X, int64_t at) {
-    Raw<F32> r;
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const char *>(X) + at * (F32 ? 4 : 2));
-    r.w[0] = p[0];
-    if (F32) r.w[F32 ? 1 : 0] = p[1];
-    return r;
-}
-
-template <bool F32>
-__device__ __forceinline__ void values(const Raw<F32> &r, float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (F32) {
-            v[j] = __uint_as_float(r.w[0][j]);
-            v[4 + j] = __uint_as_float(r.w[F32 ? 1 : 0][j]);
-        } else {
-            v[2 * j] = bf16_lo(r.w[0][j]);
-            v[2 * j + 1] = bf16_hi(r.w[0][j]);
-        }
-    }
-}
-
-__device__ __forceinline__ void load_inv(const float *lam, int k, float (&inv)[8]) {
-    const f32x4 *p = reinterpret_cast<const f32x4 *>(lam + k);
-    const f32x4 x = p[0], y = p[1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        inv[j] = 1.0f / x[j];
-        inv[4 + j] = 1.0f / y[j];
-    }
-}
-
-// rint(fl32(v inv)) as the low byte of v inv + 1.5 * 2^23 (the addition rounds
-// to the nearest integer, ties to even, for |v inv| < 2^22).
-__device__ __forceinline__ uint32_t code8(float v, float inv) {
-    return __float_as_uint(v * inv + 12582912.0f);
-}
-
-__device__ __forceinline__ u32x2 codes8(const float (&v)[8], float inv) {
-    u32x2 out;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t ab = __builtin_amdgcn_perm(code8(v[4 * h + 1], inv), code8(v[4 * h], inv), 0x0C0C0400);
-        const uint32_t cd = __builtin_amdgcn_perm(code8(v[4 * h + 3], inv), code8(v[4 * h + 2], inv), 0x04000C0C);
-        out[h] = ab | cd;
-    }
-    return out;
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
-}
 
 // The largest of `x` over the workgroup; `slot` alternates between calls, so
 // that one barrier a call is enough.
@@ -80,16 +19,6 @@ __device__ __forceinline__ float group_max(float x, float (*part)[WAVES], int sl
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) x = fmaxf(x, part[slot][w]);
     return x;
-}
-
-__device__ __forceinline__ float scale_of(float amax, float &inv) {
-    const float s = amax / 127.0f;
-    inv = 0.0f;
-    if (s != 0.0f) {
-        const float t = 1.0f / s;
-        inv = __builtin_isfinite(t) ? t : 0.0f;
-    }
-    return s;
 }
 
 // One workgroup per `rows` consecutive rows; thread t holds the pieces of 8

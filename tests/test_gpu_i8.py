@@ -197,6 +197,34 @@ def test_linear_is_its_two_steps(M, N, K, smooth, act):
     assert bool(((Y.double() - full).abs() <= 1.13 * step * 1.001 + 2.0 ** -8 * full.abs() + 1e-6).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 8, 64), (1, 40, 192), (2, 264, 2048), (4, 8192, 2048), (4, 8200, 2048),
+                                   (1, 8200, 4096), (2, 72, 2112), (3, 72, 2112), (1, 24, 8192),
+                                   (1, 1000, 8128), (3, 520, 1984), (2, 16400, 320), (1, 40000, 128),
+                                   (1, 4096, 448), (4, 32, 576), (1, 16, 8256)])
+@pytest.mark.parametrize("smooth,act", [(False, 0), (True, 1)])
+def test_linear_of_a_few_tokens(M, N, K, smooth, act):
+    """One launch or two, by the sizes: the codes, scales and sums are the same, so the outputs
+    are; nothing is written outside them."""
+    X, lam = _acts(M, K, M + N)
+    if M > 1:
+        X[1] = 0
+    if M > 3:
+        X[3] = torch.full((K,), 1e-40).to(torch.bfloat16)
+    X, lam = X.to(DEV), torch.from_numpy(lam).to(DEV) if smooth else None
+    qw, sw = _codes(N, K, N), torch.rand(N, device=DEV) * 0.02
+    bias = torch.randn(N, device=DEV).to(torch.bfloat16) if act else None
+    qa, sa = bdt.i8_quantize_act(X, lam)
+    want = bdt.i8_gemm(qa, sa, qw, sw, bias, act)
+    need = bdt.svdq_i8_linear_workspace_bytes(M, N, K)
+    for _ in range(2):
+        buf = torch.full((M * N + 512,), -777.0, dtype=torch.bfloat16, device=DEV)
+        ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+        bdt.svdq_i8_linear(X, lam, qw, sw, bias, act, M, N, K, buf[256:256 + M * N], ws[256:], need)
+        assert torch.equal(buf[256:256 + M * N].view(M, N), want)
+        assert bool((buf[:256] == -777).all()) and bool((buf[256 + M * N:] == -777).all())
+        assert bool((ws[:256] == 0x5A).all()) and bool((ws[256 + need:] == 0x5A).all())
+
+
 def test_layer_object_is_the_linear():
     g = torch.Generator(device=DEV).manual_seed(6)
     W, lam = torch.randn(72, 320, generator=g, device=DEV), 0.5 + torch.rand(320, generator=g, device=DEV)
