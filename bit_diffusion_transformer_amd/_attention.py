@@ -120,7 +120,7 @@ def rope_tables(pos: torch.Tensor, dims: Sequence[int], theta=10000.0):
     axes = rope_axes(dims, theta)
     S = expect(pos, "pos", F32, (None, axes.axes))[0]
     dev = one_device(pos=pos)
-    cos_t, sin_t = torch.empty((2, S, sum(axes.dims) // 2), dtype=torch.float32, device=dev).unbind(0)
+    cos_t, sin_t = pos.new_empty((2, S, sum(axes.dims) // 2)).unbind(0)
     with on(dev):
         svdq_rope_tables(pos, S, axes, cos_t, sin_t)
     return cos_t, sin_t
@@ -140,7 +140,7 @@ def qkv_norm_rope(qkv: torch.Tensor, heads: int, head_dim: int, seq: int, gamma_
     if seq < 1 or M % seq:
         raise ValueError("%d rows are no multiple of seq = %d" % (M, seq))
     dev = one_device(qkv=qkv, gamma_q=gamma_q, gamma_k=gamma_k, cos_t=cos_t, sin_t=sin_t)
-    out = torch.empty((3, M // seq, heads, seq, head_dim), dtype=torch.bfloat16, device=dev)
+    out = qkv.new_empty((3, M // seq, heads, seq, head_dim), dtype=torch.bfloat16)
     Q, K, V = out.unbind(0)
     at, each = out.data_ptr(), M * heads * head_dim * 2
     epi = QkvEpilogue(heads, head_dim, seq, ptr(gamma_q), ptr(gamma_k), eps, ptr(cos_t),
@@ -169,7 +169,7 @@ def select_blocks(q, k, keep: int, first: int = 0, kv_len: Optional[torch.Tensor
     the queries' mean (the first `first` always), ascending, -1 behind the last."""
     s = _shape(q, k, kv_len, keep, first)
     dev = one_device(q=q, k=k, kv_len=kv_len)
-    blocks = torch.empty(_lists(s), dtype=torch.int32, device=dev)
+    blocks = q.new_empty(_lists(s), dtype=torch.int32)
     need = svdq_select_blocks_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):
@@ -187,7 +187,7 @@ def block_attention(q, k, v, blocks, scale: Optional[float] = None,
     expect(v, "v", BF16, tuple(k.shape))
     expect(blocks, "blocks", I32, _lists(s))
     dev = one_device(q=q, k=k, v=v, blocks=blocks, kv_len=kv_len)
-    out = torch.empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16, device=dev)
+    out = q.new_empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16)
     need = svdq_block_attention_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):
@@ -204,8 +204,8 @@ def sparse_attention(q, k, v, keep: int, first: int = 0, scale: Optional[float] 
     s = _shape(q, k, kv_len, keep, first)
     expect(v, "v", BF16, tuple(k.shape))
     dev = one_device(q=q, k=k, v=v, kv_len=kv_len)
-    out = torch.empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16, device=dev)
-    blocks = torch.empty(_lists(s), dtype=torch.int32, device=dev) if return_blocks else None
+    out = q.new_empty((s.batch, s.seq_q, s.heads, s.head_dim), dtype=torch.bfloat16)
+    blocks = q.new_empty(_lists(s), dtype=torch.int32) if return_blocks else None
     need = svdq_sparse_attention_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):

@@ -94,7 +94,7 @@ def i8_gemm(qa, sa, qw, sw, bias=None, act: int = ACT_NONE,
     dev = one_device(qa=qa, sa=sa, qw=qw, sw=sw, bias=bias)
     need = svdq_i8_gemm_workspace_bytes(M, N, K)
     ws = scratch(workspace, need, dev)
-    Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    Y = qa.new_empty((M, N), dtype=torch.bfloat16)
     with on(dev):
         svdq_i8_gemm(qa, sa, qw, sw, bias, act, M, N, K, Y, ws, need)
     return Y
@@ -111,7 +111,7 @@ def i8_linear(X, lam, qw, sw, bias=None, act: int = ACT_NONE,
     dev = one_device(X=X, lam=lam, qw=qw, sw=sw, bias=bias)
     need = svdq_i8_linear_workspace_bytes(M, N, K)
     ws = scratch(workspace, need, dev)
-    Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    Y = X.new_empty((M, N), dtype=torch.bfloat16)
     with on(dev):
         svdq_i8_linear(X, lam, qw, sw, bias, act, M, N, K, Y, ws, need)
     return Y

@@ -16,22 +16,29 @@ _SAME = contextlib.nullcontext()
 def expect(t: torch.Tensor, what: str, dtypes, shape) -> torch.Size:
     """The shape of `t`, a contiguous tensor of one of `dtypes` and of `shape` (None entries
     are free)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous():
+        got = t.shape
+        if got == shape:
+            return got
+        if len(got) == len(shape):
+            for n, w in zip(got, shape):
+                if w is not None and w != n:
+                    break
+            else:
+                return got
+    _refuse(t, what, dtypes, shape)
+
+
+def _refuse(t, what, dtypes, shape):
+    """The error of a tensor that `expect` does not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a tensor, got %s" % (what, type(t).__name__))
     if t.dtype not in dtypes:
         raise TypeError("%s: expected %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
-    got = t.shape
-    fits = len(got) == len(shape)
-    if fits:
-        for n, w in zip(got, shape):
-            if w is not None and w != n:
-                fits = False
-    if not fits:
+    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
         raise ValueError("%s: expected shape %s, got %s"
-                         % (what, tuple("*" if w is None else w for w in shape), tuple(got)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return got
+                         % (what, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % what)
 
 
 BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 or its bit patterns
@@ -42,17 +49,17 @@ I32 = (torch.int32,)
 
 def one_device(**tensors: Optional[torch.Tensor]) -> torch.device:
     """The GPU that holds every given tensor (None entries are passed over)."""
-    dev = None
+    first, index = None, -1
     for what, t in tensors.items():
         if t is None:
             continue
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError("%s must be on a GPU, is on %s" % (what, t.device))
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, dev))
-    return dev
+        if first is None:
+            first, index = t, t.get_device()
+        elif t.get_device() != index:
+            raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, first.device))
+    return first.device
 
 
 def on(dev: torch.device):

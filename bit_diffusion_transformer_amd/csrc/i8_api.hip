@@ -52,6 +52,12 @@ Workspace carve(void *base, int64_t M, int64_t K) {
     return w;
 }
 
+// svdq_i8_linear's: a few tokens need none, their codes stay on the chip.
+size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N < 0 || K <= 0 || i8_few_tokens(M, N, K)) return 0;
+    return carve(nullptr, M, K).bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,8 +117,7 @@ int32_t svdq_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const 
 }
 
 size_t svdq_i8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M < 0 || N < 0 || K < 0) return 0;
-    return carve(nullptr, M, K).bytes;
+    return linear_workspace(M, N, K);
 }
 
 int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw, const float *sw,
@@ -127,7 +132,7 @@ int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw,
     SVDQ_TRY(need_ptr(sw, "sw"));
     SVDQ_TRY(need_ptr(Y, "Y"));
     if (bias) SVDQ_TRY(need_ptr(bias, "bias"));
-    SVDQ_TRY(check_workspace(workspace, ws_bytes, carve(nullptr, M, K).bytes));
+    SVDQ_TRY(check_workspace(workspace, ws_bytes, linear_workspace(M, N, K)));
     SVDQ_TRY(check_device());
     hipStream_t s = (hipStream_t)stream;
     if (i8_few_tokens(M, N, K))

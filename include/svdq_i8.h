@@ -67,11 +67,13 @@ int32_t svdq_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const 
                      const uint16_t *bias, int32_t act, int64_t M, int64_t N, int64_t K,
                      uint16_t *Y, void *workspace, size_t ws_bytes, void *stream);
 
-/* Workspace of svdq_i8_linear (qa, sa and the product's). */
+/* Workspace of svdq_i8_linear: qa and sa (0 for a few tokens, whose codes never
+ * leave the chip; `workspace` may then be NULL). */
 size_t svdq_i8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* The whole layer: svdq_i8_quantize_act, then svdq_i8_gemm on one stream,
- * intermediates carved out of `workspace`. */
+ * intermediates carved out of `workspace`; for a few tokens one launch that does
+ * both, with the same result to the bit. */
 int32_t svdq_i8_linear(const uint16_t *X, const float *lambda, const int8_t *qw, const float *sw,
                        const uint16_t *bias, int32_t act, int64_t M, int64_t N, int64_t K,
                        uint16_t *Y, void *workspace, size_t ws_bytes, void *stream);
