@@ -15,12 +15,13 @@
 //
 // 12 heads of 32760 queries, 64 of 512 blocks each, D = 128: 800-840 us, about 1
 // PFLOP/s; 48 heads of 4608, 24 of 72 blocks: 195-208 us; 24 heads of 16384, 32
-// of 256 blocks, D = 64: 262 us.  The matrix units are busy half the time, and the
-// parts add up: the two products and their LDS reads alone take 609 us where the whole takes 800
-// (at the 1.7 GHz that their power leaves), the softmax 111 more, the copies (32
-// KB per 128 x 64 scores) the rest.  Two waves share a SIMD; a wave's key block
-// costs it 790 cycles to issue copies, 770 for S, 1190 for the softmax, 1130 for
-// the second product and 130 at the barrier.
+// of 256 blocks, D = 64: 262 us.  Bound by power: all-zero inputs take 637 us for
+// the first of these, in as many cycles (1.5 million) at 2.4 GHz that random ones
+// get at 1.85.  The parts add up: the two products and their LDS reads alone take
+// 609 us where the whole takes 800, the softmax 111 more, the copies (32 KB per 128
+// x 64 scores) the rest.  Two waves share a SIMD; a wave's key block costs it 790
+// cycles to issue copies, 770 for S, 1190 for the softmax, 1130 for the second
+// product and 130 at the barrier.
 #include "attention_internal.h"
 #include "svdq_wave.h"
 

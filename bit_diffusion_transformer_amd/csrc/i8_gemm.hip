@@ -13,8 +13,8 @@
 //
 // Measured with inputs that change from call to call (operations: two per code
 // product).  4096 x 4096 -> 16384 with GELU: 263 us, 2.09 POP/s; 4608 x 12288 ->
-// 4096: 215 us, 2.16 POP/s: the matrix units' issue at the clock that their power
-// leaves.  One token, 4096 -> 24576: 18.8 us, 5.4 TB/s of weights.  333 tokens,
+// 4096: 215 us, 2.16 POP/s.  Bound by power: all-zero codes take 211 and 169 us, in
+// as many cycles at 2.45 GHz that random ones get at 1.9.  One token, 4096 -> 24576: 18.8 us, 5.4 TB/s of weights.  333 tokens,
 // 4096 -> 4096: 15 us, of which 4 are a launch with one stage; every further
 // stage of 128 costs 0.35 us (two workgroups' barrier, 32 KB of copies, 64 KB of
 // fragment reads), whether its operands are in the L2s or not.
