@@ -422,17 +422,24 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, const
 
 }  // namespace attn
 
-// Few query blocks: the lists are shared among workgroups until there are
-// about two per compute unit, four key blocks a piece at least (32 query blocks
-// of 32 key blocks: pieces of four and their join take 14.0 us, of two 14.5).
+// Few query blocks: their lists are split into pieces, of two key blocks at least,
+// for a workgroup each.  The number of pieces with the least time, in ns: a piece's
+// key blocks one after another (a second workgroup on a compute unit gains nothing:
+// both take twice as long), and the join's launch with its partial results, written
+// and read again.  16 heads, D = 128, one piece | the choice: one row, 8 and 32
+// blocks 11.9 | 9.3 and 37 | 12.5 us; 300 rows, 16 and 64 blocks 22.4 | 19.6 and 81
+// | 30 us; 60 heads of 300 rows, 8 blocks 15.9 (one piece; two take 26.8).
 int attention_splits(const AttnShape &a) {
-    const int64_t wgs = a.planes_q * a.nq;
-    if (wgs >= 256 || wgs == 0) return 1;
-    const int64_t taken = a.keep < a.nk ? a.keep : a.nk;
-    int64_t s = (512 + wgs - 1) / wgs;
-    if (s > taken / 4) s = taken / 4;
-    if (s > 32) s = 32;
-    return s < 1 ? 1 : (int)s;
+    const int64_t wgs = a.planes_q * a.nq, rows = a.planes_q * a.seq_q;
+    const int64_t taken = a.keep < a.nk ? a.keep : a.nk, each = a.D == 128 ? 1250 : 900;
+    int best = 1;
+    int64_t least = 0;
+    for (int s = 1; s <= 32 && (s == 1 || (2 * s <= taken && wgs < 256)); ++s) {
+        const int64_t full = wgs * s > 256 ? wgs * s : 256;
+        const int64_t ns = (taken + s - 1) / s * each * full / 256 + (s > 1 ? 3200 + 300 * s + rows * s * a.D / 400 : 0);
+        if (s == 1 || ns < least) best = s, least = ns;
+    }
+    return best;
 }
 
 size_t attention_workspace(const AttnShape &a) {
