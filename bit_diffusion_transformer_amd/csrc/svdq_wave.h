@@ -41,7 +41,7 @@ __device__ __forceinline__ void wait_loads() {
 // against the 64-bit form over -9 .. 9), below that of the rational erf at two
 // thirds of its issue cycles.  Past |x| = 8, where h < 2^-50, |x| is held there.
 __device__ __forceinline__ float gelu_exp2(float x) {
-    const float a = fminf(fabsf(x), 8.0f);
+    const float a = __builtin_elementwise_minimum(fabsf(x), 8.0f);   // a NaN stays one
     float p = __builtin_fmaf(a, 1.7755859516910277e-05f, -0.0006477624410763383f);
     p = __builtin_fmaf(a, p, 0.0077240546233952045f);
     p = __builtin_fmaf(a, p, -0.05292674899101257f);

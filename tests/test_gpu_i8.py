@@ -148,6 +148,27 @@ def test_gelu_epilogue_accuracy(M):
     assert bool(((Y - ref).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("M", [1, 4, 40, 300, 2100, 4096])
+def test_gelu_of_what_is_not_finite(M):
+    """NaN stays NaN, +inf stays, -inf goes to the limit 0 (held at |x| = 8, where GELU is below
+    8 2^-50); the columns beside them are untouched."""
+    K, N = 64, 2048
+    qa, qw = _codes(M, K, 3), _codes(N, K, 4)
+    sa, sw = torch.full((M,), 0.01, device=DEV), torch.full((N,), 0.01, device=DEV)
+    bias = torch.zeros(N, dtype=torch.bfloat16, device=DEV)
+    bad = bias.clone()
+    bad[5::64], bad[6::64], bad[7::64] = float("nan"), float("inf"), -float("inf")
+    X, _ = _acts(M, K, 8)
+    for run in (lambda b: bdt.i8_gemm(qa, sa, qw, sw, b, 1), lambda b: bdt.i8_linear(X.to(DEV), None, qw, sw, b, 1)):
+        Y, clean = run(bad), run(bias)
+        assert bool(Y[:, 5::64].isnan().all()) and bool((Y[:, 6::64] == float("inf")).all())
+        assert bool((Y[:, 7::64].abs() <= 8 * 2.0 ** -50).all())
+        keep = torch.ones(N, dtype=torch.bool, device=DEV)
+        for i in (5, 6, 7):
+            keep[i::64] = False
+        assert torch.equal(Y[:, keep], clean[:, keep])
+
+
 @pytest.mark.parametrize("M", [1, 16, 200, 3000])
 def test_gemm_largest_sums_are_exact(M):
     """Every code 127 at the longest K: S = 127^2 2^17, below 2^31 by less than 2 %; scales of
