@@ -94,7 +94,7 @@ int32_t check_workspace(const void *ws, size_t ws_bytes, size_t need) {
 // svdq_sparse_attention: the selection's means, or afterwards the attention's
 // partial results, and the lists.
 size_t list_bytes(const AttnShape &a) {
-    return align256((size_t)(a.planes_q * a.nq) * (size_t)a.keep * 4);
+    return a.every() ? 0 : align256((size_t)(a.planes_q * a.nq) * (size_t)a.keep * 4);
 }
 size_t step_bytes(const AttnShape &a) {
     const size_t s = select_workspace(a), t = attention_workspace(a);
@@ -179,7 +179,7 @@ int32_t svdq_block_attention(const uint16_t *q, const uint16_t *k, const uint16_
     SVDQ_TRY(need_ptr(out, "out"));
     SVDQ_TRY(check_workspace(workspace, ws_bytes, attention_workspace(a)));
     SVDQ_TRY(check_device());
-    return hip_status(launch_block_attention(q, k, v, kv_len, a, scale, blocks, out, workspace,
+    return hip_status(launch_block_attention(q, k, v, kv_len, a, scale, blocks, nullptr, out, workspace,
                                              (hipStream_t)stream),
                       "block_attention launch");
 }
@@ -207,11 +207,16 @@ int32_t svdq_sparse_attention(const uint16_t *q, const uint16_t *k, const uint16
     SVDQ_TRY(check_workspace(workspace, ws_bytes, step_bytes(a) + list_bytes(a)));
     SVDQ_TRY(check_device());
     hipStream_t s = (hipStream_t)stream;
+    if (a.every())                                   // nothing to select
+        return hip_status(launch_block_attention(q, k, v, kv_len, a, scale, nullptr, blocks, out,
+                                                 workspace, s),
+                          "block_attention launch");
     int32_t *lists = blocks ? blocks
                             : reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + step_bytes(a));
     SVDQ_TRY(hip_status(launch_select_blocks(q, k, kv_len, a, lists, workspace, s),
                         "select_blocks launch"));
-    return hip_status(launch_block_attention(q, k, v, kv_len, a, scale, lists, out, workspace, s),
+    return hip_status(launch_block_attention(q, k, v, kv_len, a, scale, lists, nullptr, out, workspace,
+                                             s),
                       "block_attention launch");
 }
 

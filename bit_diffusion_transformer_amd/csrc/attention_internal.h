@@ -27,6 +27,7 @@ struct AttnShape {
     int64_t nq, nk;               // query blocks of 128 rows, key blocks of 64
     int64_t planes_q, planes_k;   // B H, B G
     int H, G, D, keep, first;
+    bool every() const { return keep >= nk; }   // lists hold every block with a valid key
 };
 
 size_t select_workspace(const AttnShape &a);
@@ -35,9 +36,10 @@ hipError_t launch_select_blocks(const uint16_t *q, const uint16_t *k, const int3
 
 int attention_splits(const AttnShape &a);   // workgroups that share a query block's keys
 size_t attention_workspace(const AttnShape &a);
+// blocks null: every block with a valid key, the lists written to `made` unless null
 hipError_t launch_block_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                   const int32_t *kv_len, const AttnShape &a, float scale,
-                                  const int32_t *blocks, uint16_t *out, void *ws,
+                                  const int32_t *blocks, int32_t *made, uint16_t *out, void *ws,
                                   hipStream_t stream);
 
 }  // namespace svdq

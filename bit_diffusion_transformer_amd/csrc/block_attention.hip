@@ -82,10 +82,18 @@ struct Lds {
 };
 
 // The list's usable entries, in order: not negative, below `valid`, above every
-// entry before them.  By the first wave.
+// entry before them; without a list, 0 .. valid - 1, which goes to `made` (keep
+// entries) if that is given.  By the first wave.
 __device__ __forceinline__ void read_list(const int32_t *__restrict__ blocks, int keep, int valid,
-                                          uint16_t *list, int *count) {
+                                          uint16_t *list, int *count, int32_t *made) {
     const int lane = threadIdx.x & 63;
+    if (!blocks) {
+        for (int i = lane; i < valid; i += 64) list[i] = (uint16_t)i;
+        if (made)
+            for (int i = lane; i < keep; i += 64) made[i] = i < valid ? i : -1;
+        if (lane == 0) *count = valid;
+        return;
+    }
     int n = 0, top = -1;
     for (int i0 = 0; i0 < keep; i0 += 64) {
         const int e = i0 + lane < keep ? blocks[i0 + lane] : -1;
@@ -114,8 +122,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : 2)
 block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
                        const uint16_t *__restrict__ v, const int32_t *__restrict__ kv_len,
                        AttnShape a, float scale_log2, const int32_t *__restrict__ blocks,
-                       uint16_t *__restrict__ out, int splits, float *__restrict__ part,
-                       float *__restrict__ stat) {
+                       int32_t *__restrict__ made, uint16_t *__restrict__ out, int splits,
+                       float *__restrict__ part, float *__restrict__ stat) {
     constexpr int DB = D / 32, DK = D / 16;        // 32-wide blocks and 16-wide steps of D
     constexpr int RPT = 512 / D;                   // rows per 1 KB copy
     constexpr int SEGS = D / 8;                    // 16-byte segments of a row
@@ -137,7 +145,8 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
         len = n < 0 ? 0 : n > len ? len : n;
     }
     if (wave == 0)
-        read_list(blocks + id * a.keep, a.keep, (len + kKB - 1) / kKB, lds.list, lds.count());
+        read_list(blocks ? blocks + id * a.keep : nullptr, a.keep, (len + kKB - 1) / kKB, lds.list,
+                  lds.count(), made && piece == 0 ? made + id * a.keep : nullptr);
     __syncthreads();
     int first = 0, last = *lds.count();
     if (SPLIT) {
@@ -399,19 +408,19 @@ join_kernel(const float *__restrict__ part, const float *__restrict__ stat, Attn
 
 template <int D>
 hipError_t launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kv_len,
-                  const AttnShape &a, float scale, const int32_t *blocks, uint16_t *out, void *ws,
-                  hipStream_t stream) {
+                  const AttnShape &a, float scale, const int32_t *blocks, int32_t *made,
+                  uint16_t *out, void *ws, hipStream_t stream) {
     const float c = scale * 1.4426950408889634f;
     const int splits = attention_splits(a);
     const unsigned grid = (unsigned)(a.planes_q * a.nq * splits);
     if (splits == 1) {
-        block_attention_kernel<D, false><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, out,
-                                                                   1, nullptr, nullptr);
+        block_attention_kernel<D, false><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, made,
+                                                                   out, 1, nullptr, nullptr);
         return hipGetLastError();
     }
     const int64_t rows = a.planes_q * a.seq_q;
     float *part = static_cast<float *>(ws), *stat = part + rows * splits * D;
-    block_attention_kernel<D, true><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, out,
+    block_attention_kernel<D, true><<<grid, 256, 0, stream>>>(q, k, v, kv_len, a, c, blocks, made, out,
                                                               splits, part, stat);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -449,10 +458,10 @@ size_t attention_workspace(const AttnShape &a) {
 
 hipError_t launch_block_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                   const int32_t *kv_len, const AttnShape &a, float scale,
-                                  const int32_t *blocks, uint16_t *out, void *ws,
+                                  const int32_t *blocks, int32_t *made, uint16_t *out, void *ws,
                                   hipStream_t stream) {
-    return a.D == 64 ? attn::launch<64>(q, k, v, kv_len, a, scale, blocks, out, ws, stream)
-                     : attn::launch<128>(q, k, v, kv_len, a, scale, blocks, out, ws, stream);
+    return a.D == 64 ? attn::launch<64>(q, k, v, kv_len, a, scale, blocks, made, out, ws, stream)
+                     : attn::launch<128>(q, k, v, kv_len, a, scale, blocks, made, out, ws, stream);
 }
 
 }  // namespace svdq

@@ -45,7 +45,7 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 // keys), by scores | by means: 1 row 18.4 | 23.2 us, 16 rows 21.1 | 23.3 us; 64
 // rows of 24 heads (24 of keys) 67 | 38 us.
 __host__ __device__ inline bool few_queries(const AttnShape &a) {
-    return a.nq == 1 && a.nk > 0 && a.seq_q * ((a.H / a.G + 15) / 16) <= 16;
+    return a.nq == 1 && a.seq_q * ((a.H / a.G + 15) / 16) <= 16;
 }
 
 // Means over blocks of rows.  One workgroup per block of one head: 16-byte
@@ -321,6 +321,18 @@ block_choose_few_kernel(const uint64_t *__restrict__ scores, const int32_t *__re
     else choose<0>(keys, nk, valid, a.keep, threadIdx.x, out);
 }
 
+// Lists of every block with a valid key (AttnShape::every): nothing to score.
+__global__ void __launch_bounds__(256)
+every_block_kernel(const int32_t *__restrict__ kv_len, AttnShape a, int64_t entries,
+                   int32_t *__restrict__ blocks) {
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < entries; at += (int64_t)gridDim.x * 256) {
+        const int64_t list = at / a.keep;
+        const int p = (int)(at - list * a.keep);
+        const int64_t valid = (valid_keys(kv_len, list / (a.H * a.nq), a.seq_k) + kKB - 1) / kKB;
+        blocks[at] = p < valid ? p : -1;
+    }
+}
+
 namespace {
 
 // 64-bit means of a side, its blocks in tiles of 16.
@@ -340,6 +352,13 @@ int choose_rows(const AttnShape &a) {
 template <int D>
 hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, const AttnShape &a,
                   int32_t *blocks, void *ws, hipStream_t stream) {
+    if (a.every()) {
+        const int64_t entries = a.planes_q * a.nq * a.keep;
+        const int64_t wgs = (entries + 255) / 256;
+        every_block_kernel<<<(unsigned)(wgs < 2048 ? wgs : 2048), 256, 0, stream>>>(kv_len, a, entries,
+                                                                                    blocks);
+        return hipGetLastError();
+    }
     if (few_queries(a)) {
         uint64_t *scores = static_cast<uint64_t *>(ws);
         block_means_kernel<D, true><<<(unsigned)(a.planes_k * a.nk), 256, 0, stream>>>(
@@ -366,6 +385,7 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const int32_t *kv_len, c
 }  // namespace
 
 size_t select_workspace(const AttnShape &a) {
+    if (a.every()) return 0;
     if (few_queries(a)) return align256((size_t)a.planes_q * (size_t)a.nk * 8);
     return means_bytes(a.planes_q, a.nq, a.D) + means_bytes(a.planes_k, a.nk, a.D);
 }

@@ -89,7 +89,8 @@ typedef struct svdq_attention_shape {
     int32_t first;      /* 0 .. keep: the first `first` key blocks are always taken (and count) */
 } svdq_attention_shape;
 
-/* Workspace of svdq_select_blocks: the blocks' means, or their scores. */
+/* Workspace of svdq_select_blocks: the blocks' means, or their scores (0 where
+ * `keep` takes every block). */
 size_t svdq_select_blocks_workspace_bytes(const svdq_attention_shape *shape);
 
 /*
@@ -137,7 +138,8 @@ size_t svdq_sparse_attention_workspace_bytes(const svdq_attention_shape *shape);
 
 /*
  * svdq_select_blocks then svdq_block_attention on one stream.  blocks: the
- * lists (out), or NULL: they stay in the workspace.
+ * lists (out), or NULL: they stay in the workspace (where `keep` takes every
+ * block there are none, and nothing is scored).
  */
 int32_t svdq_sparse_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                               const int32_t *kv_len, const svdq_attention_shape *shape,
