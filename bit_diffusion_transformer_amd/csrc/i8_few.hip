@@ -179,7 +179,10 @@ i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
             acc = mfma_i8_32x32x32(a[3], b[3], acc);
         }
     }
-    // The waves' sums, through their own rings; the first wave scales and stores.
+    // The waves' sums, through their own rings (a wave without a stage still has its
+    // first copies on their way there); the first wave scales and stores.
+    wait_loads<0>();
+    asm volatile("" ::: "memory");
     if (wave > 0)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
