@@ -18,8 +18,8 @@ hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, c
                           uint16_t *Y, hipStream_t stream);
 int64_t i8_gemm_groups(int64_t M, int64_t N);       // workgroups at most, of 512
 
-// Quantization and product in one launch, for a few tokens (i8_few_tokens); N / 32
-// workgroups of 256.
+// Quantization and product in one launch, for a few tokens (i8_few_tokens):
+// workgroups of 256 for 32 channels each (16 up to N = 8192, 8 up to 2048).
 bool i8_few_tokens(int64_t M, int64_t N, int64_t K);
 hipError_t launch_i8_few(const uint16_t *X, const float *lambda, const int8_t *qw, const float *sw,
                          const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,
