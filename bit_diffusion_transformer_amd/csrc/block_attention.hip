@@ -445,7 +445,8 @@ int attention_splits(const AttnShape &a) {
     int64_t least = 0;
     for (int s = 1; s <= 32 && (s == 1 || (2 * s <= taken && wgs < 256)); ++s) {
         const int64_t full = wgs * s > 256 ? wgs * s : 256;
-        const int64_t ns = (taken + s - 1) / s * each * full / 256 + (s > 1 ? 3200 + 300 * s + rows * s * a.D / 400 : 0);
+        const int64_t join = s > 1 ? 3200 + 300 * s + rows * s * a.D / 400 : 0;
+        const int64_t ns = (taken + s - 1) / s * each * full / 256 + join;
         if (s == 1 || ns < least) best = s, least = ns;
     }
     return best;

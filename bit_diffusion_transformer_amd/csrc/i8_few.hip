@@ -56,8 +56,9 @@ __device__ __forceinline__ void wait_stage(int younger) {
 }
 
 // Channels are the rows of one 32 x 32 block (rows past ROWS repeat the first
-// ones), tokens its columns (those past M repeat the last one).  A wave's ring holds its own stages of the weights: no barrier in the
-// loop over K, only waits for its own copies.
+// ones), tokens its columns (those past M repeat the last one).  A wave's ring
+// holds its own stages of the weights: no barrier in the loop over K, only waits
+// for its own copies.
 template <class T, bool SMOOTH, int PIECES>
 __global__ void __launch_bounds__(kFewThreads)
 i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
@@ -67,7 +68,8 @@ i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
     extern __shared__ __align__(1024) uint8_t few[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * T::ROWS;
-    const int depth = few_ring<T>(K), ring_bytes = few_ring_bytes<T>(K), row_bytes = few_stages(K) * kRow;
+    const int depth = few_ring<T>(K), ring_bytes = few_ring_bytes<T>(K);
+    const int row_bytes = few_stages(K) * kRow;
     uint8_t *const ring = few + wave * ring_bytes;
     uint8_t *const codes = few + kFewWaves * ring_bytes;
     float *const part = reinterpret_cast<float *>(codes + M * row_bytes);   // [piece][wave]
@@ -173,8 +175,9 @@ i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
     const int token = (lane & 31) < M ? lane & 31 : M - 1;
-    const uint8_t *const b_row = codes + token * row_bytes, *const a_row = ring + (lane & (T::ROWS - 1)) * kRow;
-    const int a_swz = swz(lane & (T::ROWS - 1)), b_swz = swz(token);
+    const int channel = lane & (T::ROWS - 1);
+    const uint8_t *const b_row = codes + token * row_bytes, *const a_row = ring + channel * kRow;
+    const int a_swz = swz(channel), b_swz = swz(token);
     i32x16 acc = {};
     for (int slot = 0, s = wave; s < ns; slot = slot + 1 < depth ? slot + 1 : 0, s += kFewWaves) {
         // this stage has landed when at most the younger ones remain in flight
