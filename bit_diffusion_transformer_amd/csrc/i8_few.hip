@@ -17,7 +17,7 @@ namespace svdq {
 namespace i8 {
 
 constexpr int kFewWaves = 4;                     // share K, a stage each in turn
-constexpr int kFewPieces = 4;                    // of 8 values, that a thread quantizes, at most
+constexpr int kFewPieces = 8;                    // of 8 values, that a thread quantizes, at most
 constexpr int kFewThreads = 64 * kFewWaves;
 
 // A workgroup's channels; a wave's stages in flight at most, and their copies.
@@ -244,9 +244,11 @@ static int64_t few_pieces(int64_t M, int64_t K) {
 
 // Up to two pieces a thread, or four while there are few channels to repeat them
 // for: 4 tokens, 2048 -> 4096: 7.0 us here, 8.2 in two launches, but 1024 -> 24576 with
-// smoothing 11.9 and 11.1; eight pieces, 8 tokens, 2048 -> 4096: 9.2 and 8.5.
+// smoothing 11.9 and 11.1.  Eight pieces where few channels meet a long K, whose
+// codes are long in a second launch: 2 tokens, 8192 -> 4096: 12.1 and 14.6, but 8
+// tokens, 2048 -> 4096: 9.2 and 8.5.
 bool i8_few_tokens(int64_t M, int64_t N, int64_t K) {
-    return few_pieces(M, K) <= (N <= 8192 ? kFewPieces : 2);
+    return few_pieces(M, K) <= (N > 8192 ? 2 : N <= 4096 && K > 4096 ? kFewPieces : 4);
 }
 
 template <class T, int PIECES>
@@ -268,6 +270,10 @@ hipError_t launch_i8_few(const uint16_t *X, const float *lambda, const int8_t *q
         f(X, lambda, qw, sw, bias, act, M, N, K, Y, stream);
         return hipGetLastError();
     };
+    if (pieces > 4) {
+        start_few<Few<16>, kFewPieces>(X, lambda, qw, sw, bias, act, M, N, K, Y, stream);
+        return hipGetLastError();
+    }
     // A compute unit streams at most 24 GB/s from memory, so few channels are spread
     // over more of them; more workgroups repeat the quantization, and more pieces of
     // it.  One token, 8 | 16 | 32 channels a workgroup: 1024 -> 1024 3.8 | 4.1 | 4.8 us,

@@ -317,6 +317,7 @@ hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, c
     if (tiles<Small>(M, N) <= 2 * cus) return run(Small());
     if (4 * tiles<Mid>(M, N) < 3 * cus) return run(Half());
     if (tiles<Mid>(M, N) <= cus) return run(Mid());
+    if (tiles<Half>(M, N) <= 2 * cus) return run(Half());   // 4128 x 960 x 3584: 23.5, Tall 30.0
     // Tall tiles: the height with the shortest time for the whole rounds of
     // compute units that its tiles take; a round costs its rows and, for filling
     // the ring and the epilogue, as much as 112 rows at K = 4096.

@@ -223,7 +223,9 @@ def test_linear_is_its_two_steps(M, N, K, smooth, act):
                                    (1, 1000, 8128), (3, 520, 1984), (2, 16400, 320), (1, 40000, 128),
                                    (1, 4096, 448), (4, 32, 576), (1, 16, 8256), (1, 2040, 2048), (1, 2056, 2048),
                                    (1, 2048, 2112), (4, 4096, 1024), (4, 4104, 1024), (2, 8184, 3968),
-                                   (1, 8, 7680), (3, 8, 1728), (1, 4096, 7552)])
+                                   (1, 8, 7680), (3, 8, 1728), (1, 4096, 7552), (1, 4096, 16384),
+                                   (1, 72, 16448), (2, 136, 8192), (2, 4104, 8192), (2, 520, 4160),
+                                   (4, 264, 4096)])
 @pytest.mark.parametrize("smooth,act", [(False, 0), (True, 1)])
 def test_linear_of_a_few_tokens(M, N, K, smooth, act):
     """One launch or two, by the sizes: the codes, scales and sums are the same, so the outputs
