@@ -3,6 +3,7 @@ raw calls with the C names and argument order, and the tensor-level functions on
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -113,14 +114,26 @@ def rope_axes(dims: Sequence[int], theta=10000.0) -> RopeAxes:
     return a
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_division(dims, theta):
+    """(RopeAxes, pairs of a token) of one division of the head: the same at every call."""
+    axes = rope_axes(dims, theta)
+    return axes, sum(axes.dims) // 2
+
+
 def rope_tables(pos: torch.Tensor, dims: Sequence[int], theta=10000.0):
     """Positions fp32 [S, axes] -> (cos, sin) fp32 [S, sum(dims)/2], as linear_qkv and
     qkv_norm_rope take them.  Axis a turns dims[a] elements of each head; theta: one number,
     or one per axis."""
-    axes = rope_axes(dims, theta)
+    dims = tuple(dims)
+    if isinstance(theta, (int, float)):
+        axes, pairs = _rope_division(dims, theta)
+    else:
+        axes = rope_axes(dims, theta)
+        pairs = sum(axes.dims) // 2
     S = expect(pos, "pos", F32, (None, axes.axes))[0]
     dev = one_device(pos=pos)
-    cos_t, sin_t = pos.new_empty((2, S, sum(axes.dims) // 2)).unbind(0)
+    cos_t, sin_t = pos.new_empty((2, S, pairs)).unbind(0)
     with on(dev):
         svdq_rope_tables(pos, S, axes, cos_t, sin_t)
     return cos_t, sin_t
