@@ -342,10 +342,14 @@ size_t means_bytes(int64_t planes, int64_t blocks, int D) {
 
 // Query blocks per workgroup: their keys fit 64 KB of LDS (two workgroups per
 // compute unit; 128 KB for the longest sequences).  The matrix instruction
-// takes 16 rows whatever R is: with 8 where 16 leave compute units without a
-// workgroup, 12 heads of 256 x 512 blocks took 34 us instead of 24.
+// takes 16 rows whatever R is, so 8 of them cost twice the products: 34 us instead
+// of 24 for 12 heads of 256 x 512 blocks.  But a wave then chooses for one query
+// block instead of two, and where there is a compute unit for every workgroup that
+// counts: means and choice of 8 heads of 235 x 469 blocks 43 us instead of 48, of 48
+// heads of 36 x 72 30.7 instead of 32.7.
 int choose_rows(const AttnShape &a) {
-    const int R = a.nk <= 512 ? 16 : a.nk <= 1024 ? 8 : 4;
+    int R = a.nk <= 512 ? 16 : a.nk <= 1024 ? 8 : 4;
+    if (R == 16 && a.planes_q * ((a.nq + 7) / 8) <= 256) R = 8;
     return (int)(R < a.nq ? R : a.nq);
 }
 
