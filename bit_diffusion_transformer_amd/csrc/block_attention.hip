@@ -399,9 +399,11 @@ join_kernel(const float *__restrict__ part, const float *__restrict__ stat, Attn
 #pragma unroll
         for (int d = LANES / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
         const float m1 = fmaxf(m, top);
-        if (m1 == -__builtin_inff()) continue;     // no key in any of them
-        const float f = __builtin_amdgcn_exp2f((m - m1) * scale_log2);
-        const float w = __builtin_amdgcn_exp2f((s.x - m1) * scale_log2);
+        // No maximum yet: pieces without a key, whose sums are zero, or the NaN sums of a
+        // query that is not finite, which have to stay.
+        const bool none = m1 == -__builtin_inff();
+        const float f = none ? 1.0f : __builtin_amdgcn_exp2f((m - m1) * scale_log2);
+        const float w = none ? 1.0f : __builtin_amdgcn_exp2f((s.x - m1) * scale_log2);
         m = m1;
         l = l * f + w * s.y;                       // this lane's pieces; summed below
         o *= f;

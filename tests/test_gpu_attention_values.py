@@ -17,6 +17,7 @@ import torch
 import bit_diffusion_transformer_amd as bdt
 from bit_diffusion_transformer_amd import _attention
 from tests.helpers import DEV
+from tests.test_gpu_sparse_attention import attention_64, check, inputs
 
 pytestmark = pytest.mark.gpu
 KB = 64
@@ -103,3 +104,22 @@ def test_a_common_offset_of_the_scores_changes_nothing(D, Sq, keep, n, split, of
     assert bool((tol < w / 16).all())
     err = (out.double() - o).abs()
     assert bool((err <= tol).all()), "worst %.3g of the bound" % float((err / tol).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,keep,n,split", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_row_that_is_not_finite_gives_nan(D, Sq, keep, n, split, bad):
+    """And only that row; without any key it gives zeros like every other."""
+    H, Sk = 2, keep * KB
+    q, k, v = inputs(1, H, H, D, Sq, Sk, 11)
+    row = Sq // 2
+    clean = q.clone()
+    q[0, 1, row] = bad
+    out = _attend(q, k, v, keep, n, D ** -0.5, split)
+    assert bool(out[0, row, 1].isnan().all())
+    out[0, row, 1] = 0
+    ref, tol = attention_64(clean, k, v, _every(1, H, Sq, keep).cpu(), D ** -0.5, [n])
+    ref[0, row, 1], tol[0, row, 1] = 0, 0
+    check(out, ref, tol, "the other rows")
+    assert bool((_attend(q, k, v, keep, 0, D ** -0.5, split) == 0).all())
