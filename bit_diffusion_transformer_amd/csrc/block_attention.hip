@@ -157,8 +157,9 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
 
     const uint8_t *kb = reinterpret_cast<const uint8_t *>(k + kplane * a.seq_k * D);
     const uint8_t *vb = reinterpret_cast<const uint8_t *>(v + kplane * a.seq_k * D);
-    // Rows at or past the sequence's length re-read its last valid row: their
-    // scores are masked, and their weights are zeros times finite values.
+    // Rows at or past the sequence's length are not read: K is left as it is (its scores
+    // are masked, whatever they are), V is zero (the weights are zero, and zero times
+    // what is not finite would be NaN).
     const int cp_row = wave * COPIES * RPT + lane / SEGS, cp_slot = lane % SEGS;
     uint32_t k_at[COPIES], v_at[COPIES];           // byte offsets within a block
 #pragma unroll
@@ -182,9 +183,12 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
 #pragma unroll
             for (int c = 0; c < COPIES; ++c) {
                 const int row = cp_row + c * RPT;
-                const uint32_t back = row < left ? 0 : (uint32_t)(row - left + 1) * (D * 2);
-                copy16_to_lds(k0 + (k_at[c] - back), kd + c * 1024);
-                copy16_to_lds(v0 + (v_at[c] - back), vd + c * 1024);
+                if (row < left) {
+                    copy16_to_lds(k0 + k_at[c], kd + c * 1024);
+                    copy16_to_lds(v0 + v_at[c], vd + c * 1024);
+                } else {
+                    *reinterpret_cast<u32x4 *>(vd + c * 1024 + lane * 16) = u32x4{};
+                }
             }
         }
     };

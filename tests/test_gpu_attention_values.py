@@ -1,4 +1,5 @@
-"""Block attention where the answer is known beforehand.
+"""Block attention where the answer is known beforehand: scores of any magnitude, query rows
+that are not finite, values that are not finite.
 
 Large scores.  Every score is exact in fp32 (one power of two times a small whole number, or
 sums of whole numbers below 2^24), so softmax(scale s) has no error to inherit from s, however
@@ -123,3 +124,22 @@ def test_a_query_row_that_is_not_finite_gives_nan(D, Sq, keep, n, split, bad):
     ref[0, row, 1], tol[0, row, 1] = 0, 0
     check(out, ref, tol, "the other rows")
     assert bool((_attend(q, k, v, keep, 0, D ** -0.5, split) == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,keep,n,split", FORMS)
+def test_an_infinite_value_of_the_last_key(D, Sq, keep, n, split):
+    """v of the last key infinite in some columns: so is the output there, whatever lies behind
+    the sequence's length; a NaN gives NaN; the other columns do not change."""
+    H, Sk = 2, keep * KB
+    q, k, v = inputs(1, H, H, D, Sq, Sk, 12)
+    q[...] = 0                                                    # every key counts
+    clean = _attend(q, k, v, keep, n, 1.0, split)
+    v[:, :, n:] = float("nan")
+    v[:, :, n - 1, 3], v[:, :, n - 1, 40], v[:, :, n - 1, 63] = float("inf"), -float("inf"), float("nan")
+    out = _attend(q, k, v, keep, n, 1.0, split)
+    assert bool((out[..., 3] == float("inf")).all()) and bool((out[..., 40] == -float("inf")).all())
+    assert bool(out[..., 63].isnan().all())
+    rest = torch.ones(D, dtype=torch.bool, device=DEV)
+    rest[[3, 40, 63]] = False
+    assert torch.equal(out[..., rest], clean[..., rest])
