@@ -81,22 +81,27 @@ __device__ __forceinline__ u32x2 codes8(const float (&v)[8], float inv) {
     return out;
 }
 
+// The larger of two magnitudes; a NaN stays one (and the row's outputs with it).
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 // The largest x of the wave, every lane getting it: lane exchanges within 16
 // lanes, then the swaps with the lanes 16 and 32 away.
 __device__ __forceinline__ float wave_max(float x) {
-    auto with = [&](int y) { x = fmaxf(x, __int_as_float(y)); };
+    auto with = [&](int y) { x = larger(x, __int_as_float(y)); };
     with(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, true));    // lane ^ 1
     with(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, true));    // lane ^ 2
     with(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, true));   // 7 - lane
     with(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, true));   // 15 - lane
     const uint32_t u = __float_as_uint(x);
     const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    x = larger(__uint_as_float(p[0]), __uint_as_float(p[1]));
     const uint32_t v = __float_as_uint(x);
     const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+    return larger(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
+// A NaN or an infinity in the row: not finite either, with all-zero codes (inv is 0,
+// and a NaN's code8 is 0), so the outputs are 0 times the scale, NaN.
 __device__ __forceinline__ float scale_of(float amax, float &inv) {
     const float s = amax / 127.0f;
     inv = 0.0f;

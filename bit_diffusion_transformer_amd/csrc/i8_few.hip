@@ -146,7 +146,7 @@ i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
         value(c, v[SMOOTH ? c : 0]);
         top[c] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top[c] = fmaxf(top[c], fabsf(v[SMOOTH ? c : 0][j]));
+        for (int j = 0; j < 8; ++j) top[c] = larger(top[c], fabsf(v[SMOOTH ? c : 0][j]));
         top[c] = wave_max(k < K ? top[c] : 0.0f);
     });
     if (lane == 0)
@@ -157,7 +157,7 @@ i8_few_kernel(const uint16_t *__restrict__ X, const float *__restrict__ lam,
         float top = 0.0f;
         for (int i = row * P; i < (row + 1) * P; ++i) {
             const f32x4 x = *reinterpret_cast<const f32x4 *>(part + i * kFewWaves);
-            top = fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), top);
+            top = larger(larger(larger(x.x, x.y), larger(x.z, x.w)), top);
         }
         return scale_of(top, inv);
     };

@@ -17,7 +17,7 @@ __device__ __forceinline__ float group_max(float x, float (*part)[WAVES], int sl
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = x;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) x = fmaxf(x, part[slot][w]);
+    for (int w = 0; w < WAVES; ++w) x = larger(x, part[slot][w]);
     return x;
 }
 
@@ -59,7 +59,7 @@ i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ lam, in
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (SMOOTH) v[c][j] *= inv[SMOOTH ? c : 0][j];
-                    amax = fmaxf(amax, fabsf(v[c][j]));
+                    amax = larger(amax, fabsf(v[c][j]));
                 }
             }
         }
@@ -97,7 +97,7 @@ i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ la
     for (int k = 8 * (int)threadIdx.x; k < K; k += 8 * kLong) {
         load(k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        for (int j = 0; j < 8; ++j) amax = larger(amax, fabsf(v[j]));
     }
     amax = group_max<kLong / 64>(amax, part, 0);
     float r;

@@ -8,6 +8,9 @@
  * symmetric codes in [-127, 127]:
  *   s = fl32(max|v| / 127) over the row, code = rint(fl32(v fl32(1/s))) (ties
  *   to even); s == 0, or a 1/s that is not finite, gives all-zero codes.
+ * A row with a NaN or an infinity gets all-zero codes and a scale that is not
+ * finite, so its outputs (a token's row, a channel's column of Y) are NaN; the
+ * other rows do not change.
  * The activations may be smoothed first (v = fl32(x fl32(1/lambda)), as in
  * svdq_quantize_act_down).  The products are summed exactly in 32-bit
  * integers (K <= SVDQ_I8_MAX_K keeps every sum below 2^31).
@@ -28,8 +31,7 @@ extern "C" {
 
 /*
  * Offline weight preparation (nn.Linear orientation).
- *   W   device fp32 [N, K]  finite (a NaN or an infinity gives unspecified
- *                           codes and scales)
+ *   W   device fp32 [N, K]
  *   qw  device int8 [N, K]  row-major codes (out)
  *   sw  device fp32 [N]     channel scales (out)
  * N >= 0 (0: no-op), K % 64 == 0, 64 <= K <= SVDQ_I8_MAX_K.  Codes and scales
@@ -40,8 +42,9 @@ int32_t svdq_i8_pack_weights(const float *W, int64_t N, int64_t K, int8_t *qw, f
 
 /*
  * Activation quantization, one scale per token.
- *   X       device bf16 [M, K]  finite
- *   lambda  device fp32 [K] smoothing factors (finite and > 0), or NULL: none
+ *   X       device bf16 [M, K]
+ *   lambda  device fp32 [K] smoothing factors (finite and > 0, 1/lambda finite), or
+ *                              NULL: none
  *   qa      device int8 [M, K] (out)
  *   sa      device fp32 [M] (out)
  * M >= 0 (0: no-op), K as above.  Bit-exact with the definition.
