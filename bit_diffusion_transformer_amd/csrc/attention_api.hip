@@ -78,9 +78,10 @@ int32_t read_shape(const svdq_attention_shape *e, AttnShape &a) {
 
 bool empty(const AttnShape &a) { return a.planes_q == 0 || a.seq_q == 0; }
 
+// 2^127 at most: the kernels take scale log2(e), which has to be finite.
 int32_t check_scale(float scale) {
-    if (!(scale > 0.0f) || !std::isfinite(scale))
-        return fail(SVDQ_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!(scale > 0.0f) || scale > 0x1p127f)
+        return fail(SVDQ_ERR_INVALID_ARG, "scale must be > 0 and at most 2^127");
     return SVDQ_OK;
 }
 

@@ -117,7 +117,9 @@ size_t svdq_block_attention_workspace_bytes(const svdq_attention_shape *shape);
 /*
  * Attention over given lists (shape's `first` is not read).
  *   v       device bf16 [B, G, Sk, D]
- *   scale   finite and > 0 (usually D^-1/2); |scale q[m] . k[n]| below 2^126
+ *   scale   > 0 and at most 2^127 (usually D^-1/2); the sum of |q[m][d] k[n][d]|
+ *           over d, and scale times it, below 2^126 (a larger one may pass
+ *           what fp32 holds and give NaN)
  *   blocks  device int32 [B, H, ceil(Sq/128), keep]: an entry that is
  *           negative, past the last block with a valid key, or not above
  *           every entry before it in its list is passed over, so a block

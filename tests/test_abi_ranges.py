@@ -1,0 +1,26 @@
+"""Arguments at the edges of the documented ranges: refused or taken before any device call.
+The fake pointers are never dereferenced: a call that is taken ends at the device check of a
+host without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import bit_diffusion_transformer_amd as bdt
+from bit_diffusion_transformer_amd import _attention, _binding
+
+OK, INVALID, SHAPE, MISALIGNED, WS_SMALL, NODEV, HIPERR = range(7)
+A, P = 0x10000, ctypes.c_void_p
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the taken calls would launch")
+
+
+@no_gpu
+@pytest.mark.parametrize("scale,code", [(2.0 ** 127, NODEV), (1.8e38, INVALID), (3e38, INVALID),
+                                        (1e-45, NODEV)])
+def test_scale_of_the_attention(scale, code):
+    """scale log2 e has to be finite too: an infinite one would make every weight NaN."""
+    fn, s = _attention._entries, bdt.AttentionShape(2, 200, 300, 4, 2, 128, 3, 1)
+    for name in ("svdq_block_attention", "svdq_sparse_attention"):
+        got = fn[name](P(A), P(A), P(A), P(0), ctypes.byref(s), scale, P(A), P(A), P(A), 1 << 40, None)
+        assert got == code, name
+        assert _binding.svdq_last_error()
