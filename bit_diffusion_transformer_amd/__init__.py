@@ -37,6 +37,7 @@ from ._attention import (EXPORTS_ATTENTION, AttentionShape, KEY_BLOCK, QUERY_BLO
                          svdq_block_attention_workspace_bytes, svdq_qkv_norm_rope,
                          svdq_rope_tables, svdq_select_blocks, svdq_select_blocks_workspace_bytes,
                          svdq_sparse_attention, svdq_sparse_attention_workspace_bytes)
+from ._tensors import BF16, F32, I32, U8, expect, on, one_device
 from ._int8 import (EXPORTS_I8, I8Linear, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
                     i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,
                     svdq_i8_linear_workspace_bytes, svdq_i8_pack_weights, svdq_i8_quantize_act)
@@ -252,19 +253,51 @@ def mlp(X, up: dict, down: dict, act: int = ACT_GELU,
     return Y
 
 
+def _expect_layer(layer: dict, what: str, K: int, N: Optional[int]) -> dict:
+    """The tensors of a W4A4 layer K -> N (N None: what its scales say), checked, by name."""
+    N = expect(layer["sw"], what + " sw", F32, (scale_shape(0, K)[0], N, 2))[1]
+    expect(layer["lam"], what + " lam", F32, (K,))
+    expect(layer["qw"], what + " qw", U8, (pair_rows(N), K))
+    names = ["sw", "lam", "qw"]
+    if layer.get("bias") is not None:
+        expect(layer["bias"], what + " bias", BF16, (N,))
+        names.append("bias")
+    r = _rank(layer["L1"], 1)
+    if r > 0 or _rank(layer["L2"], 0) > 0:
+        expect(layer["L1"], what + " L1", BF16, (K, r))
+        expect(layer["L2"], what + " L2", BF16, (r, N))
+        names += ["L1", "L2"]
+    return {what + " " + n: layer[n] for n in names}
+
+
 def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamma_q, gamma_k,
               eps: float, cos_t, sin_t, keep: int, first: int = 0,
               kv_len: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = out(sparse_attention(qkv(X))): the attention half of a block on two W4A4 layers
     (dicts with lam, L1, qw, sw, L2, bias), through svdq_linear_qkv, svdq_sparse_attention and
-    svdq_linear.  X bf16 [M, K], M = B seq; cos_t, sin_t from rope_tables; keep, first and
-    kv_len as for sparse_attention."""
-    Q, Kt, V = linear_qkv(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"],
-                          qkv.get("bias"), heads, head_dim, seq, gamma_q, gamma_k, eps, cos_t,
-                          sin_t)
-    A = sparse_attention(Q, Kt, V, keep, first=first, kv_len=kv_len)
-    return linear(A.view(X.shape[0], heads * head_dim), out["lam"], out["L1"], out["qw"],
-                  out["sw"], out["L2"], out.get("bias"))
+    svdq_linear.  X bf16 [M, K], M = B seq; cos_t, sin_t from rope_tables (at least seq rows);
+    keep, first and kv_len as for sparse_attention.  Every tensor is checked first."""
+    M, K = expect(X, "X", BF16, (None, None))
+    HD = heads * head_dim
+    tensors = {**_expect_layer(qkv, "qkv", K, 3 * HD), **_expect_layer(out, "out", HD, None)}
+    for what, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        expect(g, what, BF16, (head_dim,))
+    for what, t in (("cos_t", cos_t), ("sin_t", sin_t)):
+        if expect(t, what, F32, (None, head_dim // 2))[0] < seq:
+            raise ValueError("%s: expected a shape of at least %d rows" % (what, seq))
+    if seq < 1 or M % seq:
+        raise ValueError("%d rows are no multiple of seq = %d" % (M, seq))
+    if kv_len is not None:
+        expect(kv_len, "kv_len", I32, (M // seq,))
+    dev = one_device(X=X, gamma_q=gamma_q, gamma_k=gamma_k, cos_t=cos_t, sin_t=sin_t,
+                     kv_len=kv_len, **tensors)
+    with on(dev):
+        Q, Kt, V = linear_qkv(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"],
+                              qkv.get("bias"), heads, head_dim, seq, gamma_q, gamma_k, eps, cos_t,
+                              sin_t)
+        A = sparse_attention(Q, Kt, V, keep, first=first, kv_len=kv_len)
+        return linear(A.view(M, HD), out["lam"], out["L1"], out["qw"], out["sw"], out["L2"],
+                      out.get("bias"))
 
 
 def group_sums(qa, sa, qw, sw, M: int, N: int, m0: int, n0: int, tm: int,

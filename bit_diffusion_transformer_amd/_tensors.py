@@ -44,6 +44,7 @@ def _refuse(t, what, dtypes, shape):
 BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 or its bit patterns
 F32 = (torch.float32,)
 I8 = (torch.int8,)
+U8 = (torch.uint8,)
 I32 = (torch.int32,)
 
 
