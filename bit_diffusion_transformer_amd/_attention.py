@@ -9,8 +9,8 @@ from typing import Optional, Sequence
 import torch
 
 from ._binding import QkvEpilogue
-from ._tensors import (BF16, Entries, F32, F32T, I32, I32T, I64, P, SZ, expect, on, one_device,
-                       ptr, scratch, stream_ptr)
+from ._tensors import (BF16, Entries, F32, F32T, I32, I32T, I64, P, SZ, at, expect, on,
+                       one_device, ptr, scratch, stream_ptr)
 
 ROPE_MAX_AXES = 4
 QUERY_BLOCK, KEY_BLOCK = 128, 64
@@ -135,7 +135,8 @@ def rope_tables(pos: torch.Tensor, dims: Sequence[int], theta=10000.0):
     dev = one_device(pos=pos)
     cos_t, sin_t = pos.new_empty((2, S, pairs)).unbind(0)
     with on(dev):
-        svdq_rope_tables(pos, S, axes, cos_t, sin_t)
+        _entries.call("svdq_rope_tables", at(pos), S, ctypes.byref(axes), at(cos_t), at(sin_t),
+                      stream_ptr())
     return cos_t, sin_t
 
 
@@ -155,11 +156,11 @@ def qkv_norm_rope(qkv: torch.Tensor, heads: int, head_dim: int, seq: int, gamma_
     dev = one_device(qkv=qkv, gamma_q=gamma_q, gamma_k=gamma_k, cos_t=cos_t, sin_t=sin_t)
     out = qkv.new_empty((3, M // seq, heads, seq, head_dim), dtype=torch.bfloat16)
     Q, K, V = out.unbind(0)
-    at, each = out.data_ptr(), M * heads * head_dim * 2
-    epi = QkvEpilogue(heads, head_dim, seq, ptr(gamma_q), ptr(gamma_k), eps, ptr(cos_t),
-                      ptr(sin_t), at, at + each, at + 2 * each)
+    to, each = out.data_ptr(), M * heads * head_dim * 2
+    epi = QkvEpilogue(heads, head_dim, seq, at(gamma_q), at(gamma_k), eps, at(cos_t),
+                      at(sin_t), to, to + each, to + 2 * each)
     with on(dev):
-        svdq_qkv_norm_rope(qkv, M, epi)
+        _entries.call("svdq_qkv_norm_rope", at(qkv), M, ctypes.byref(epi), stream_ptr())
     return Q, K, V
 
 
@@ -186,7 +187,8 @@ def select_blocks(q, k, keep: int, first: int = 0, kv_len: Optional[torch.Tensor
     need = svdq_select_blocks_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):
-        svdq_select_blocks(q, k, kv_len, s, blocks, ws, need)
+        _entries.call("svdq_select_blocks", at(q), at(k), at(kv_len), ctypes.byref(s), at(blocks),
+                      at(ws), need, stream_ptr())
     return blocks
 
 
@@ -204,8 +206,9 @@ def block_attention(q, k, v, blocks, scale: Optional[float] = None,
     need = svdq_block_attention_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):
-        svdq_block_attention(q, k, v, kv_len, s, s.head_dim ** -0.5 if scale is None else scale,
-                             blocks, out, ws, need)
+        _entries.call("svdq_block_attention", at(q), at(k), at(v), at(kv_len), ctypes.byref(s),
+                      s.head_dim ** -0.5 if scale is None else scale, at(blocks), at(out), at(ws),
+                      need, stream_ptr())
     return out
 
 
@@ -222,6 +225,7 @@ def sparse_attention(q, k, v, keep: int, first: int = 0, scale: Optional[float] 
     need = svdq_sparse_attention_workspace_bytes(s)
     ws = scratch(workspace, need, dev)
     with on(dev):
-        svdq_sparse_attention(q, k, v, kv_len, s, s.head_dim ** -0.5 if scale is None else scale,
-                              blocks, out, ws, need)
+        _entries.call("svdq_sparse_attention", at(q), at(k), at(v), at(kv_len), ctypes.byref(s),
+                      s.head_dim ** -0.5 if scale is None else scale, at(blocks), at(out), at(ws),
+                      need, stream_ptr())
     return (out, blocks) if return_blocks else out

@@ -7,8 +7,8 @@ from typing import Optional
 import torch
 
 from ._binding import ACT_NONE
-from ._tensors import (BF16, Entries, F32, I32T, I64, I8, P, SZ, expect, on, one_device, ptr,
-                       scratch, stream_ptr)
+from ._tensors import (BF16, Entries, F32, I32T, I64, I8, P, SZ, at, expect, on, one_device,
+                       ptr, scratch, stream_ptr)
 
 _entries = Entries({
     "svdq_i8_pack_weights": ([P, I64, I64, P, P, P], I32T),
@@ -60,7 +60,7 @@ def i8_pack_weights(W: torch.Tensor):
     qw = torch.empty((N, K), dtype=torch.int8, device=dev)
     sw = torch.empty(N, dtype=torch.float32, device=dev)
     with on(dev):
-        svdq_i8_pack_weights(W, N, K, qw, sw)
+        _entries.call("svdq_i8_pack_weights", at(W), N, K, at(qw), at(sw), stream_ptr())
     return qw, sw
 
 
@@ -73,7 +73,7 @@ def i8_quantize_act(X: torch.Tensor, lam: Optional[torch.Tensor] = None):
     qa = torch.empty((M, K), dtype=torch.int8, device=dev)
     sa = torch.empty(M, dtype=torch.float32, device=dev)
     with on(dev):
-        svdq_i8_quantize_act(X, lam, M, K, qa, sa)
+        _entries.call("svdq_i8_quantize_act", at(X), at(lam), M, K, at(qa), at(sa), stream_ptr())
     return qa, sa
 
 
@@ -96,7 +96,8 @@ def i8_gemm(qa, sa, qw, sw, bias=None, act: int = ACT_NONE,
     ws = scratch(workspace, need, dev)
     Y = qa.new_empty((M, N), dtype=torch.bfloat16)
     with on(dev):
-        svdq_i8_gemm(qa, sa, qw, sw, bias, act, M, N, K, Y, ws, need)
+        _entries.call("svdq_i8_gemm", at(qa), at(sa), at(qw), at(sw), at(bias), act, M, N, K, at(Y),
+                      at(ws), need, stream_ptr())
     return Y
 
 
@@ -113,7 +114,8 @@ def i8_linear(X, lam, qw, sw, bias=None, act: int = ACT_NONE,
     ws = scratch(workspace, need, dev)
     Y = X.new_empty((M, N), dtype=torch.bfloat16)
     with on(dev):
-        svdq_i8_linear(X, lam, qw, sw, bias, act, M, N, K, Y, ws, need)
+        _entries.call("svdq_i8_linear", at(X), at(lam), at(qw), at(sw), at(bias), act, M, N, K,
+                      at(Y), at(ws), need, stream_ptr())
     return Y
 
 

@@ -68,8 +68,18 @@ def on(dev: torch.device):
     return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def ptr(t: Optional[torch.Tensor]):
+def at(t: Optional[torch.Tensor]):
+    """The address of a tensor that `expect` has seen, or None."""
     return None if t is None else t.data_ptr()
+
+
+def ptr(t: Optional[torch.Tensor]):
+    """The address of a tensor, which has to be contiguous, or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libsvdq must be contiguous")
+    return t.data_ptr()
 
 
 # The current stream's handle alone; torch.cuda.current_stream makes an object of it, which

@@ -24,3 +24,28 @@ def test_scale_of_the_attention(scale, code):
         got = fn[name](P(A), P(A), P(A), P(0), ctypes.byref(s), scale, P(A), P(A), P(A), 1 << 40, None)
         assert got == code, name
         assert _binding.svdq_last_error()
+
+
+def test_raw_calls_refuse_tensors_that_are_not_contiguous():
+    """The pointer alone does not tell the strides: like the raw calls of svdq.h, these raise
+    before they reach the library."""
+    t = torch.zeros(8, 8).t()
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_i8_pack_weights(t, 8, 8, None, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_i8_quantize_act(None, t, 8, 64, None, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_i8_gemm(None, None, t, None, None, 0, 8, 8, 64, None, None, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_i8_linear(None, None, None, None, None, 0, 8, 8, 64, None, t, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_rope_tables(t, 8, bdt.rope_axes((64,)), None, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_qkv_norm_rope(t, 8, _binding.QkvEpilogue())
+    s = bdt.AttentionShape(1, 8, 8, 1, 1, 64, 1, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_select_blocks(None, t, None, s, None, None, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_block_attention(None, None, t, None, s, 1.0, None, None, None, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        bdt.svdq_sparse_attention(None, None, None, None, s, 1.0, None, t, None, 0)
