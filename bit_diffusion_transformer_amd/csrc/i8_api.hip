@@ -16,6 +16,10 @@ int32_t check_k_i8(int64_t K) {
     return SVDQ_OK;
 }
 
+int32_t check_quantizer(int64_t rows, int64_t K, const char *what) {
+    return check_grid(i8_quantize_groups(rows, K), i8_quantize_threads(K), what);
+}
+
 int32_t check_shape(int32_t act, int64_t M, int64_t N, int64_t K) {
     SVDQ_TRY(check_rows(M, "M"));
     if (act != SVDQ_ACT_NONE && act != SVDQ_ACT_GELU)
@@ -24,7 +28,7 @@ int32_t check_shape(int32_t act, int64_t M, int64_t N, int64_t K) {
     SVDQ_TRY(check_k_i8(K));
     if (M == 0) return SVDQ_OK;
     SVDQ_TRY(check_grid(i8_gemm_groups(M, N), 512, "the 8-bit GEMM"));
-    return check_grid(i8_quantize_groups(M), 512, "the 8-bit quantizer");
+    return check_quantizer(M, K, "the 8-bit quantizer");
 }
 
 int32_t check_workspace(const void *ws, size_t ws_bytes, size_t need) {
@@ -68,7 +72,7 @@ int32_t svdq_i8_pack_weights(const float *W, int64_t N, int64_t K, int8_t *qw, f
     SVDQ_TRY(check_rows(N, "N"));
     SVDQ_TRY(check_k_i8(K));
     if (N == 0) return SVDQ_OK;
-    SVDQ_TRY(check_grid(i8_quantize_groups(N), 512, "the 8-bit packer"));
+    SVDQ_TRY(check_quantizer(N, K, "the 8-bit packer"));
     SVDQ_TRY(need_ptr(W, "W"));
     SVDQ_TRY(need_ptr(qw, "qw"));
     SVDQ_TRY(need_ptr(sw, "sw"));
@@ -83,7 +87,7 @@ int32_t svdq_i8_quantize_act(const uint16_t *X, const float *lambda, int64_t M, 
     SVDQ_TRY(check_rows(M, "M"));
     SVDQ_TRY(check_k_i8(K));
     if (M == 0) return SVDQ_OK;
-    SVDQ_TRY(check_grid(i8_quantize_groups(M), 512, "the 8-bit quantizer"));
+    SVDQ_TRY(check_quantizer(M, K, "the 8-bit quantizer"));
     SVDQ_TRY(need_ptr(X, "X"));
     if (lambda) SVDQ_TRY(need_ptr(lambda, "lambda"));
     SVDQ_TRY(need_ptr(qa, "qa"));

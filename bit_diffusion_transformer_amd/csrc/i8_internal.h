@@ -11,7 +11,8 @@ namespace svdq {
 // `fp32`, fp32 rows without smoothing -> codes [M, K] and scales [M]
 hipError_t launch_i8_quantize(const void *X, bool fp32, const float *lambda, int64_t M, int64_t K,
                               int8_t *q, float *s, hipStream_t stream);
-int64_t i8_quantize_groups(int64_t M);   // workgroups at most, of 512
+int64_t i8_quantize_groups(int64_t M, int64_t K);   // workgroups, and their threads
+int64_t i8_quantize_threads(int64_t K);
 
 hipError_t launch_i8_gemm(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw,
                           const uint16_t *bias, int act, int64_t M, int64_t N, int64_t K,

@@ -75,8 +75,9 @@ i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ lam, in
     }
 }
 
-// Rows too long for the registers (K > 16384): the row is read twice (the
-// second time mostly from the caches).
+// Rows too long for the registers: the row is read twice (the second time mostly
+// from the caches).
+constexpr int kMaxRegisters = 16384;
 constexpr int kLong = 512;
 
 template <bool F32>
@@ -133,14 +134,18 @@ hipError_t launch(const void *X, const float *lam, int64_t M, int64_t K, int8_t 
     else if (K <= 4096) start<256, 2, F32>(X, lam, M, K, q, s, stream);
     else if (K <= 8192) start<512, 2, F32>(X, lam, M, K, q, s, stream);
     else if (K <= 12288) start<512, 3, F32>(X, lam, M, K, q, s, stream);
-    else if (K <= 16384) start<512, 4, F32>(X, lam, M, K, q, s, stream);
+    else if (K <= kMaxRegisters) start<512, 4, F32>(X, lam, M, K, q, s, stream);
     else i8_quantize_long_kernel<F32><<<(unsigned)M, kLong, 0, stream>>>(X, lam, K, q, s);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t i8_quantize_groups(int64_t M) { return M; }
+int64_t i8_quantize_groups(int64_t M, int64_t K) {
+    const int rows = K > kMaxRegisters ? 1 : rows_per_group(M);
+    return (M + rows - 1) / rows;
+}
+int64_t i8_quantize_threads(int64_t K) { return K <= 4096 ? 256 : 512; }
 
 hipError_t launch_i8_quantize(const void *X, bool fp32, const float *lambda, int64_t M, int64_t K,
                               int8_t *q, float *s, hipStream_t stream) {

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import bit_diffusion_transformer_amd as bdt
-from bit_diffusion_transformer_amd import _attention, _binding
+from bit_diffusion_transformer_amd import _attention, _binding, _int8
 
 OK, INVALID, SHAPE, MISALIGNED, WS_SMALL, NODEV, HIPERR = range(7)
 A, P = 0x10000, ctypes.c_void_p
@@ -49,3 +49,17 @@ def test_raw_calls_refuse_tensors_that_are_not_contiguous():
         bdt.svdq_block_attention(None, None, t, None, s, 1.0, None, None, None, 0)
     with pytest.raises(ValueError, match="contiguous"):
         bdt.svdq_sparse_attention(None, None, None, None, s, 1.0, None, t, None, 0)
+
+
+@no_gpu
+@pytest.mark.parametrize("rows,K,code", [
+    (1 << 23, 64, NODEV), ((1 << 26) - 4, 4096, NODEV), ((1 << 26) + 4, 4096, SHAPE),
+    ((1 << 25) - 4, 8192, NODEV), ((1 << 25) + 4, 8192, SHAPE),
+    ((1 << 23) - 1, 16448, NODEV), (1 << 23, 16448, SHAPE)])
+def test_rows_of_the_8bit_quantizer(rows, K, code):
+    """As many as its launch takes: four a workgroup of 256 (512 from K = 4160 on), one of 512
+    past K = 16384; 2^32 - 1 work-items."""
+    fn = _int8._entries
+    assert fn["svdq_i8_quantize_act"](P(A), P(0), rows, K, P(A), P(A), None) == code
+    assert fn["svdq_i8_pack_weights"](P(A), rows, K, P(A), P(A), None) == code
+    assert fn["svdq_i8_linear"](P(A), P(0), P(A), P(A), P(0), 0, rows, 8, K, P(A), P(A), 1 << 60, None) == code

@@ -52,3 +52,15 @@ def test_a_channel_that_is_not_finite(N, K, bad):
     Y = bdt.i8_linear(X, None, *bdt.i8_pack_weights(W))
     keep = torch.arange(N, device=DEV) != 7
     assert bool(Y[:, 7].isnan().all()) and torch.equal(Y[:, keep], clean[:, keep])
+
+
+def test_more_than_2_to_the_23_rows():
+    """Each row for itself: slices from both ends and the middle, quantized alone, agree."""
+    M, K = (1 << 23) + 5, 64
+    g = torch.Generator(device=DEV).manual_seed(1)
+    X = torch.randn(M, K, generator=g, device=DEV, dtype=torch.float32).to(torch.bfloat16)
+    qa, sa = bdt.i8_quantize_act(X)
+    for at in (0, (1 << 22) - 100, (1 << 23) - 100, M - 300):
+        q, s = bdt.i8_quantize_act(X[at:at + 300])
+        assert torch.equal(qa[at:at + 300], q) and torch.equal(sa[at:at + 300], s)
+    assert bool((sa > 0).all())
