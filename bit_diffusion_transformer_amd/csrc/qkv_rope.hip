@@ -15,7 +15,7 @@ constexpr int kPairs = SVDQ_ROPE_MAX_DIM / 2;
 // by the stores of both tables, 8 bytes a pair (118800 tokens of 64 pairs: 14.3
 // us, 4.3 TB/s; 4608 tokens: 3.7 us, the launch and one pass of the sines).  The angle is taken in turns
 // in 64 bits, t = pos (f / 2 pi), and loses its whole turns there (an exact
-// step), so a position past 10^6 keeps about 2^-32 of a turn; what is left,
+// step), so a position of 2^26 keeps 2^-27 of a turn; what is left,
 // at most half a turn, fits fp32 and goes through the fp32 sine and cosine of
 // a multiple of pi.  The pairs' frequencies are formed once per workgroup (a
 // 64-bit exponential each), then 16 lanes (D = 128) write a token's row in

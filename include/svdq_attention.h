@@ -49,8 +49,10 @@ typedef struct svdq_rope_axes {
  *   cos_t  device fp32 [S, D/2]    (out)
  *   sin_t  device fp32 [S, D/2]    (out)
  * S >= 0 (0: no-op).  Angles are formed in 64 bits and reduced to one turn
- * there, so positions past 10^6 keep their accuracy; sine and cosine of the
- * reduced angle in fp32: absolute error at most 2^-21.
+ * there; sine and cosine of the reduced angle in fp32: absolute error at most
+ * 2^-21 for |pos| <= 2^26 and theta >= 1.  Farther positions add up to
+ * 7 |pos| 2^-53, the rounding of the frequencies (2^-21 in all is passed near
+ * 2^31); with theta < 1 the frequencies, and that error, grow with 1 / theta.
  */
 int32_t svdq_rope_tables(const float *pos, int64_t S, const svdq_rope_axes *axes, float *cos_t,
                          float *sin_t, void *stream);
