@@ -64,3 +64,16 @@ def test_more_than_2_to_the_23_rows():
         q, s = bdt.i8_quantize_act(X[at:at + 300])
         assert torch.equal(qa[at:at + 300], q) and torch.equal(sa[at:at + 300], s)
     assert bool((sa > 0).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(4128, 960, 320), (4128, 952, 64), (9300, 440, 192)])
+@pytest.mark.parametrize("act", [0, 1])
+def test_gemm_where_two_narrow_tiles_fit_a_compute_unit(M, N, K, act):
+    """Tiles of 128 x 128 just miss one for each compute unit, those of 128 x 64 fit twice."""
+    from tests.test_gpu_i8 import _codes, check_y, y_64
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    qa, qw = _codes(M, K, 1), _codes(N, K, 2)
+    sa, sw = torch.rand(M, generator=g, device=DEV) * 0.02, torch.rand(N, generator=g, device=DEV) * 0.02
+    bias = torch.randn(N, generator=g, device=DEV).to(torch.bfloat16)
+    ref, mag = y_64(qa, sa, qw, sw, bias, act)
+    check_y(bdt.i8_gemm(qa, sa, qw, sw, bias, act), ref, mag, act, "M%d N%d K%d" % (M, N, K))
