@@ -121,8 +121,8 @@ def i8_linear(X, lam, qw, sw, bias=None, act: int = ACT_NONE,
 
 class I8Linear:
     """An 8-bit replacement for one linear layer, beside SVDQLinear for the layers that lose
-    too much in 4 bits: ``from_weight`` packs the weight (and the smoothing factors' inverse
-    into it) on the GPU once, ``__call__`` runs the layer."""
+    too much in 4 bits: ``from_weight`` packs the weight (times the smoothing factors that the
+    activations are divided by) on the GPU once, ``__call__`` runs the layer."""
 
     def __init__(self, lam, qw, sw, bias=None, act: int = ACT_NONE):
         self.lam, self.qw, self.sw, self.bias, self.act = lam, qw, sw, bias, act

@@ -13,13 +13,13 @@
 // while the current one is used); K is read in 16-byte pieces, V through the
 // transposing 8-byte LDS read.
 //
-// 12 heads of 32760 queries, 64 of 512 blocks each, D = 128: 800-840 us, about 1
-// PFLOP/s; 48 heads of 4608, 24 of 72 blocks: 195-208 us; 24 heads of 16384, 32
-// of 256 blocks, D = 64: 262 us.  Bound by power: all-zero inputs take 637 us for
-// the first of these, in as many cycles (1.5 million) at 2.4 GHz that random ones
-// get at 1.85.  The parts add up: the two products and their LDS reads alone take
-// 609 us where the whole takes 800, the softmax 111 more, the copies (32 KB per 128
-// x 64 scores) the rest.  Two waves share a SIMD; a wave's key block costs it 790
+// Calls in a row, on several cards.  12 heads of 32760 queries, 64 of 512 blocks each,
+// D = 128: 810-870 us, 0.95-1.02 PFLOP/s; 48 heads of 4608, 24 of 72 blocks: 190-204
+// us; 24 heads of 16384, 32 of 256 blocks, D = 64: 248-252 us.  Bound by power:
+// all-zero inputs take 637 us for the first of these, in as many cycles (1.5 million)
+// at 2.4 GHz that random ones get at 1.85.  The parts add up: on a card where the whole
+// takes 800 us, the two products and their LDS reads alone take 609, the softmax 111
+// more, the copies (32 KB per 128 x 64 scores) the rest.  Two waves share a SIMD; a wave's key block costs it 790
 // cycles to issue copies, 770 for S, 1190 for the softmax, 1130 for the second
 // product and 130 at the barrier.
 #include "attention_internal.h"
@@ -312,7 +312,12 @@ block_attention_kernel(const uint16_t *__restrict__ q, const uint16_t *__restric
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[kk][e] -= by;
         }
-        u32x4 p[2][2];                             // [kk][step of 16 keys]: weights in bf16
+        // [kk][step of 16 keys]: weights, rounded to bf16, the type of the matrix instruction's
+        // operand beside V.  Rounded once, and the same values go into their sum, so a row's
+        // weights still add up to one; the output's error against 64 bits is 0.0023 of its
+        // size instead of 0.0017, which its own rounding to bf16 makes.  (A second product of
+        // what the rounding leaves would take half as much time again in the products.)
+        u32x4 p[2][2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
@@ -457,7 +462,9 @@ hipError_t launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, const
 // both take twice as long), and the join's launch with its partial results, written
 // and read again.  16 heads, D = 128, one piece | the choice: one row, 8 and 32
 // blocks 11.9 | 9.3 and 37 | 12.5 us; 300 rows, 16 and 64 blocks 22.4 | 19.6 and 81
-// | 30 us; 60 heads of 300 rows, 8 blocks 15.9 (one piece; two take 26.8).
+// | 30 us; 60 heads of 300 rows, 8 blocks 15.9 (one piece; two take 26.8).  256 is
+// the whole card's compute units, not the current device's: the workspace's size
+// follows from the result, and has to be the same wherever it is asked for.
 int attention_splits(const AttnShape &a) {
     const int64_t wgs = a.planes_q * a.nq, rows = a.planes_q * a.seq_q;
     const int64_t taken = a.keep < a.nk ? a.keep : a.nk, each = a.D == 128 ? 1250 : 900;

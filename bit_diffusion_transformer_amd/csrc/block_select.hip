@@ -53,7 +53,7 @@ __host__ __device__ inline bool few_queries(const AttnShape &a) {
 // the threads of a wave and, through LDS, over the waves.  Bound by reading Q and
 // K once.  Stored in the order in which the score kernel's matrix
 // instruction takes them (mean_at), so that each of its loads is one run.
-// 12 heads of 32760 x 128, Q and K: 38 us, 5.3 TB/s.
+// 12 heads of 32760 x 128, Q and K: 46 us, 4.4 TB/s; 48 heads of 4608: 28 us.
 //
 // FEW: one query block of few rows (few_queries).  Workgroups for key blocks
 // only; LANES threads a query head then sum its rows, and the block's scores go
@@ -235,7 +235,7 @@ __device__ __forceinline__ void choose(const uint64_t *kr, int nk, int valid, in
 // registers throughout, tiles of key blocks shared among the waves; the order
 // of k is free, so a lane takes two neighbouring columns in one 16-byte load.
 // The keys go to LDS, where a wave then chooses for each of its query blocks.
-// 12 heads of 256 x 512 blocks: 24.8 us, of which the choice takes 10 (about 18
+// 12 heads of 256 x 512 blocks: 26 us, of which the choice takes 10 (about 18
 // bits, eight ballots each), the products 5 and their loads 5; 48 heads of 36 x
 // 72 blocks: 9.8 us.
 template <int D>
@@ -346,7 +346,8 @@ size_t means_bytes(int64_t planes, int64_t blocks, int D) {
 // of 24 for 12 heads of 256 x 512 blocks.  But a wave then chooses for one query
 // block instead of two, and where there is a compute unit for every workgroup that
 // counts: means and choice of 8 heads of 235 x 469 blocks 43 us instead of 48, of 48
-// heads of 36 x 72 30.7 instead of 32.7.
+// heads of 36 x 72 30.7 instead of 32.7.  (256: the whole card's; a partition with
+// fewer would choose 16 rows earlier, with the same lists.)
 int choose_rows(const AttnShape &a) {
     int R = a.nk <= 512 ? 16 : a.nk <= 1024 ? 8 : 4;
     if (R == 16 && a.planes_q * ((a.nq + 7) / 8) <= 256) R = 8;

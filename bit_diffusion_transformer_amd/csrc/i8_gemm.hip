@@ -11,13 +11,13 @@
 // (exact: K <= 2^17).  The epilogue scales in fp32, adds the bias, applies
 // the activation and rounds once.
 //
-// Measured with inputs that change from call to call (operations: two per code
-// product).  4096 x 4096 -> 16384 with GELU: 263 us, 2.09 POP/s; 4608 x 12288 ->
-// 4096: 215 us, 2.16 POP/s.  Bound by power: all-zero codes take 211 and 169 us, in
-// as many cycles at 2.45 GHz that random ones get at 1.9.  One token, 4096 -> 24576: 18.8 us, 5.4 TB/s of weights.  333 tokens,
-// 4096 -> 4096: 15 us, of which 4 are a launch with one stage; every further
-// stage of 128 costs 0.35 us (two workgroups' barrier, 32 KB of copies, 64 KB of
-// fragment reads), whether its operands are in the L2s or not.
+// Measured by calls in a row with inputs that change (operations: two per code
+// product).  4096 x 4096 -> 16384 with GELU: 260-263 us, 2.1 POP/s; 4608 x 12288 ->
+// 4096: 200-206 us, 2.25-2.3 POP/s.  Bound by power: all-zero codes take 211 and 169
+// us, in as many cycles at 2.45 GHz that random ones get at 1.9.  333 tokens, 4096 ->
+// 4096: 14.5 us, of which 4 are a launch with one stage; every further stage of 128
+// costs 0.35 us (two workgroups' barrier, 32 KB of copies, 64 KB of fragment reads),
+// whether its operands are in the L2s or not.
 #include "i8_device.h"
 #include "i8_internal.h"
 #include "svdq_wave.h"

@@ -27,7 +27,8 @@ __device__ __forceinline__ float group_max(float x, float (*part)[WAVES], int sl
 // rows (a correctly rounded division costs about as much as everything else
 // here together).  The next row is loaded before the current one is reduced.
 // Bound by memory: 2 bytes read and 1 written per element (4 and 1 for W).
-// 4608 x 12288 with smoothing: 32.7 us, 5.2 TB/s; 333 x 4096: 3.7 us.
+// 4608 x 12288 with smoothing: 36 us, 4.7 TB/s; 333 x 4096: 3.5 us; weights of 16384 x
+// 4096: 66 us, 5.1 TB/s.
 template <int THREADS, int CH, bool F32, bool SMOOTH>
 __global__ void __launch_bounds__(THREADS)
 i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ lam, int64_t M, int64_t K,

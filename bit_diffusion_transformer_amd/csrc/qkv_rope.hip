@@ -13,7 +13,7 @@ constexpr int kPairs = SVDQ_ROPE_MAX_DIM / 2;
 
 // cos_t[s][p], sin_t[s][p] of angle pos[s][axis(p)] theta^(-2 i / dims): bound
 // by the stores of both tables, 8 bytes a pair (118800 tokens of 64 pairs: 14.3
-// us, 4.3 TB/s; 4608 tokens: 3.7 us, the launch and one pass of the sines).  The angle is taken in turns
+// us, 4.3 TB/s; 4608 tokens: 3.5 us, the launch and one pass of the sines).  The angle is taken in turns
 // in 64 bits, t = pos (f / 2 pi), and loses its whole turns there (an exact
 // step), so a position of 2^26 keeps 2^-27 of a turn; what is left,
 // at most half a turn, fits fp32 and goes through the fp32 sine and cosine of
@@ -74,8 +74,8 @@ constexpr int kStep = 256 * kPer;      // pieces per workgroup
 // one head, so a head is 8 or 16 neighbouring lanes, its sum of squares is
 // three or four lane exchanges, and loads and stores are 16 bytes wide and
 // contiguous over a head's row.  A thread's four pieces are loaded before the
-// first is used.  4608 tokens of 24 heads of 128: 37.7 us, 4.5 TB/s; 9003 tokens
-// of 18 heads of 64: 26.2 us, 4.7 TB/s; one token: 3.5 us, the launch.
+// first is used.  4608 tokens of 24 heads of 128: 37.5 us, 4.6 TB/s; 9003 tokens
+// of 18 heads of 64: 26.1 us, 4.8 TB/s; one token: 3.2 us, the launch.
 template <int D>
 __global__ void __launch_bounds__(256)
 qkv_norm_rope_kernel(const uint16_t *__restrict__ qkv, int64_t M, QkvArgs a) {
