@@ -50,13 +50,12 @@ def mx_scale_rows(rows: int) -> int:
     return (int(rows) + 15) // 16 * 16
 
 
+_BF16 = frozenset(BF16)
+
+
 def _bits(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    """bf16 tensor -> the same storage viewed as int16 (no copy)."""
-    if t is None:
-        return None
-    if t.dtype == torch.bfloat16:
-        return t.view(torch.int16)
-    if t.dtype in (torch.int16, torch.uint16):
+    """A bf16 tensor or its 16-bit pattern, for the raw calls: they take its address alone."""
+    if t is None or t.dtype in _BF16:
         return t
     raise TypeError("expected bf16 (or its 16-bit pattern), got %s" % t.dtype)
 
@@ -253,21 +252,28 @@ def mlp(X, up: dict, down: dict, act: int = ACT_GELU,
     return Y
 
 
+_LAYERS = {what: tuple(what + " " + n for n in ("sw", "lam", "qw", "bias", "L1", "L2"))
+           for what in ("qkv", "out")}
+
+
 def _expect_layer(layer: dict, what: str, K: int, N: Optional[int]) -> dict:
     """The tensors of a W4A4 layer K -> N (N None: what its scales say), checked, by name."""
-    N = expect(layer["sw"], what + " sw", F32, (scale_shape(0, K)[0], N, 2))[1]
-    expect(layer["lam"], what + " lam", F32, (K,))
-    expect(layer["qw"], what + " qw", U8, (pair_rows(N), K))
-    names = ["sw", "lam", "qw"]
-    if layer.get("bias") is not None:
-        expect(layer["bias"], what + " bias", BF16, (N,))
-        names.append("bias")
-    r = _rank(layer["L1"], 1)
-    if r > 0 or _rank(layer["L2"], 0) > 0:
-        expect(layer["L1"], what + " L1", BF16, (K, r))
-        expect(layer["L2"], what + " L2", BF16, (r, N))
-        names += ["L1", "L2"]
-    return {what + " " + n: layer[n] for n in names}
+    n_sw, n_lam, n_qw, n_bias, n_L1, n_L2 = _LAYERS[what]
+    sw, lam, qw, bias = layer["sw"], layer["lam"], layer["qw"], layer.get("bias")
+    N = expect(sw, n_sw, F32, ((K // GROUP + 1) // 2, N, 2))[1]
+    expect(lam, n_lam, F32, (K,))
+    expect(qw, n_qw, U8, (pair_rows(N), K))
+    tensors = {n_sw: sw, n_lam: lam, n_qw: qw}
+    if bias is not None:
+        expect(bias, n_bias, BF16, (N,))
+        tensors[n_bias] = bias
+    L1, L2 = layer["L1"], layer["L2"]
+    r = _rank(L1, 1)
+    if r > 0 or _rank(L2, 0) > 0:
+        expect(L1, n_L1, BF16, (K, r))
+        expect(L2, n_L2, BF16, (r, N))
+        tensors[n_L1], tensors[n_L2] = L1, L2
+    return tensors
 
 
 def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamma_q, gamma_k,
@@ -279,18 +285,20 @@ def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamm
     keep, first and kv_len as for sparse_attention.  Every tensor is checked first."""
     M, K = expect(X, "X", BF16, (None, None))
     HD = heads * head_dim
-    tensors = {**_expect_layer(qkv, "qkv", K, 3 * HD), **_expect_layer(out, "out", HD, None)}
-    for what, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
-        expect(g, what, BF16, (head_dim,))
-    for what, t in (("cos_t", cos_t), ("sin_t", sin_t)):
-        if expect(t, what, F32, (None, head_dim // 2))[0] < seq:
+    expect(gamma_q, "gamma_q", BF16, (head_dim,))
+    expect(gamma_k, "gamma_k", BF16, (head_dim,))
+    tensors = {"X": X, "gamma_q": gamma_q, "gamma_k": gamma_k, "cos_t": cos_t, "sin_t": sin_t,
+               **_expect_layer(qkv, "qkv", K, 3 * HD), **_expect_layer(out, "out", HD, None)}
+    for what in ("cos_t", "sin_t"):
+        if expect(tensors[what], what, F32, (None, head_dim // 2))[0] < seq:
             raise ValueError("%s: expected a shape of at least %d rows" % (what, seq))
     if seq < 1 or M % seq:
         raise ValueError("%d rows are no multiple of seq = %d" % (M, seq))
     if kv_len is not None:
         expect(kv_len, "kv_len", I32, (M // seq,))
-    dev = one_device(X=X, gamma_q=gamma_q, gamma_k=gamma_k, cos_t=cos_t, sin_t=sin_t,
-                     kv_len=kv_len, **tensors)
+        tensors["kv_len"] = kv_len
+    one = len({t.get_device() for t in tensors.values()}) == 1
+    dev = one_device(X=X) if one else one_device(**tensors)     # the latter raises
     with on(dev):
         Q, Kt, V = linear_qkv(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"],
                               qkv.get("bias"), heads, head_dim, seq, gamma_q, gamma_k, eps, cos_t,

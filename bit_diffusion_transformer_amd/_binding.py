@@ -133,7 +133,7 @@ def _p(t: Optional[torch.Tensor]):
 
 def _stream(stream=None):
     if stream is None:
-        if not torch.cuda.is_available():
+        if not torch.cuda.is_initialized() and not torch.cuda.is_available():
             return None
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)

@@ -111,3 +111,16 @@ def test_every_step_runs_on_the_tensors_device(monkeypatch):
     monkeypatch.setattr(bdt, "linear", step("out", torch.zeros(B * S, N, dtype=bf)))
     assert bdt.attention(**_args()).shape == (B * S, N)
     assert ran == [(n, ["the device"]) for n in ("qkv", "attention", "out")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["X", "cos_t", "gamma_k", "kv_len", "qkv", "out"])
+def test_a_tensor_left_on_the_host_is_refused(nothing_launched, name):
+    def up(v):
+        if isinstance(v, dict):
+            return {n: up(t) for n, t in v.items()}
+        return v.cuda() if isinstance(v, torch.Tensor) else v
+    args = _args()
+    args = {n: v if n == name else up(v) for n, v in args.items()}
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        bdt.attention(**args)
