@@ -130,9 +130,10 @@ size_t svdq_block_attention_workspace_bytes(const svdq_attention_shape *shape);
  *           projection
  * Products in bf16 with fp32 sums; the softmax in fp32 with the running
  * maximum and sum; its weights are rounded once to bf16 for the product with
- * v; one rounding of the result to bf16.  A query row, or a valid key, that is
- * not finite gives NaN in the rows it takes part in, an infinite valid v an
- * infinite or NaN column; other rows do not see it.
+ * v; one rounding of the result to bf16.  A NaN or an infinity in a query row
+ * gives a row of NaN, a NaN in a valid key NaN in the rows that take it, an
+ * infinite valid v an infinity (or NaN beside weights of zero) in its column;
+ * other rows do not see them.
  */
 int32_t svdq_block_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                              const int32_t *kv_len, const svdq_attention_shape *shape,

@@ -143,3 +143,18 @@ def test_an_infinite_value_of_the_last_key(D, Sq, keep, n, split):
     rest = torch.ones(D, dtype=torch.bool, device=DEV)
     rest[[3, 40, 63]] = False
     assert torch.equal(out[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,keep,n,split", FORMS)
+def test_a_key_that_is_nan(D, Sq, keep, n, split):
+    """NaN in every row of its head (all take it), in no row of the other; behind the length it
+    takes no part."""
+    H, Sk = 2, keep * KB
+    q, k, v = inputs(1, H, H, D, Sq, Sk, 13)
+    clean = _attend(q, k, v, keep, n, D ** -0.5, split)
+    k[:, :, n:] = float("nan")
+    assert torch.equal(_attend(q, k, v, keep, n, D ** -0.5, split), clean)
+    k[0, 1, n // 2, 9] = float("nan")
+    out = _attend(q, k, v, keep, n, D ** -0.5, split)
+    assert bool(out[:, :, 1].isnan().all()) and torch.equal(out[:, :, 0], clean[:, :, 0])
