@@ -13,15 +13,16 @@
 // while the current one is used); K is read in 16-byte pieces, V through the
 // transposing 8-byte LDS read.
 //
-// Calls in a row, on several cards.  12 heads of 32760 queries, 64 of 512 blocks each,
-// D = 128: 810-870 us, 0.95-1.02 PFLOP/s; 48 heads of 4608, 24 of 72 blocks: 190-204
-// us; 24 heads of 16384, 32 of 256 blocks, D = 64: 248-252 us.  Bound by power:
-// all-zero inputs take 637 us for the first of these, in as many cycles (1.5 million)
-// at 2.4 GHz that random ones get at 1.85.  The parts add up: on a card where the whole
-// takes 800 us, the two products and their LDS reads alone take 609, the softmax 111
-// more, the copies (32 KB per 128 x 64 scores) the rest.  Two waves share a SIMD; a wave's key block costs it 790
-// cycles to issue copies, 770 for S, 1190 for the softmax, 1130 for the second
-// product and 130 at the barrier.
+// Calls in a row, on two cards.  12 heads of 32760 queries, 64 of 512 blocks each, D =
+// 128: 854-870 us, 0.95-0.97 PFLOP/s (a faster card takes 5 % less with its selection);
+// 48 heads of 4608, 24 of 72 blocks: 198-204 us; 24 heads of 16384, 32 of 256 blocks,
+// D = 64: 248-252 us.  Bound by power: all-zero inputs take 637 us for the first of
+// these, in as many cycles (1.5 million) at 2.4 GHz that random ones get at 1.85.  The
+// parts add up: on a card where the whole takes 800 us, the two products and their LDS
+// reads alone take 609, the softmax 111 more, the copies (32 KB per 128 x 64 scores)
+// the rest.  Two waves share a SIMD; a wave's key block costs it 790 cycles to issue
+// copies, 770 for S, 1190 for the softmax, 1130 for the second product and 130 at the
+// barrier.
 #include "attention_internal.h"
 #include "svdq_wave.h"
 
