@@ -37,6 +37,11 @@ from ._attention import (EXPORTS_ATTENTION, AttentionShape, KEY_BLOCK, QUERY_BLO
                          svdq_block_attention_workspace_bytes, svdq_qkv_norm_rope,
                          svdq_rope_tables, svdq_select_blocks, svdq_select_blocks_workspace_bytes,
                          svdq_sparse_attention, svdq_sparse_attention_workspace_bytes)
+from ._paged import (CacheEpilogue, EXPORTS_PAGED, PackedShape, PagedShape, TableShape,  # noqa: F401
+                     packed_attention, page_tables, paged_attention, qkv_norm_rope_cache,
+                     svdq_packed_attention, svdq_packed_attention_workspace_bytes,
+                     svdq_page_tables, svdq_paged_attention,
+                     svdq_paged_attention_workspace_bytes, svdq_qkv_norm_rope_cache)
 from ._tensors import BF16, F32, I32, U8, expect, on, one_device
 from ._int8 import (EXPORTS_I8, I8Linear, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
                     i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,

@@ -41,6 +41,23 @@ def _refuse(t, what, dtypes, shape):
     raise ValueError("%s must be contiguous" % what)
 
 
+def expect_rows(t: torch.Tensor, what: str, dtypes, shape):
+    """(shape, elements from one row to the next) of `t`, a tensor of one of `dtypes` and of
+    `shape` (None entries are free) whose rows are contiguous but may lie apart (a part of a
+    projection's columns)."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3 and not t.is_contiguous():
+        _, n, m = t.shape
+        s = t.stride()
+        if (m <= 1 or s[2] == 1) and (n <= 1 or s[1] == m) and s[0] >= n * m:
+            rows, n_want, m_want = shape
+            if (t.dtype not in dtypes or rows not in (None, t.shape[0]) or n_want not in (None, n)
+                    or m_want not in (None, m)):
+                _refuse(t, what, dtypes, shape)
+            return t.shape, s[0]
+    got = expect(t, what, dtypes, shape)
+    return got, got[1] * got[2]
+
+
 BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 or its bit patterns
 F32 = (torch.float32,)
 I8 = (torch.int8,)

@@ -3,7 +3,7 @@
 // that the fused QKV epilogue of w4a4_tile.h does on its own tile, for the
 // GEMMs without one).
 #include "attention_internal.h"
-#include "svdq_device.h"
+#include "svdq_wave.h"
 
 namespace svdq {
 
@@ -50,19 +50,6 @@ rope_tables_kernel(const float *__restrict__ pos, int64_t S, RopeAxes ax, int pa
         *reinterpret_cast<f32x4 *>(cos_t + s * pairs + p) = c;
         *reinterpret_cast<f32x4 *>(sin_t + s * pairs + p) = d;
     }
-}
-
-// Sum over the LPH (8 or 16) consecutive lanes that share a head, every lane
-// getting it: the quad, then its mirror in 8 lanes, then in 16.
-template <int LPH>
-__device__ __forceinline__ float head_sum(float x) {
-    auto add = [&](int ctrl_applied) { x += __int_as_float(ctrl_applied); };
-    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, true));    // lane ^ 1
-    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, true));    // lane ^ 2
-    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, true));   // 7 - lane
-    if (LPH == 16)
-        add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, true));   // 15 - lane
-    return x;
 }
 
 constexpr int kPer = 4;                // 16-byte pieces per thread

@@ -1,0 +1,516 @@
+// span_attention.hip -- attention of packed sequences and of new tokens over a
+// paged cache, on the bf16 matrix instruction (v_mfma_f32_32x32x16_bf16).
+//
+// A tile is 128 rows of one sequence and key head: row r is head r % group of
+// token r / group, so that the heads that share a key head share its tiles, and
+// a few tokens fill more of one.  Four waves of 32 rows go over the tile's
+// blocks of 64 keys with the score and weight layouts of the block-sparse
+// kernel: S^T = K Q^T, the softmax within a lane, O^T = V^T P^T, K and V copied
+// into LDS a block ahead.  What a workgroup does is a piece of the line of all
+// tiles (span_plan.h).
+#include "attention_tile.h"
+#include "span_plan.h"
+
+#include <type_traits>
+
+namespace svdq {
+
+namespace span {
+
+using namespace attn;
+
+constexpr int kRows = 128;
+
+template <int D>
+struct Lds {
+    static constexpr int TILE = kKeys * D * 2;     // bytes of a K or V block
+    uint8_t k[2][TILE];
+    uint8_t v[2][TILE];
+};
+
+// The workspace: shared tiles' headers (one a worker), then partial results, two
+// slots a worker: 2 w + 1 for the tile that begins in its piece and ends
+// outside, 2 w for the one that began before.
+__host__ __device__ inline size_t header_bytes(int workers) { return align256((size_t)workers * sizeof(Shared)); }
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(256, D == 64 ? 4 : 2)
+span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict__ part,
+                      float *__restrict__ stat) {
+    constexpr int DB = D / 32, DK = D / 16;        // 32-wide blocks and 16-wide steps of D
+    constexpr int RPT = 512 / D;                   // rows per 1 KB copy
+    constexpr int SEGS = D / 8;                    // 16-byte segments of a row
+    constexpr int COPIES = kKeys / RPT / 4;        // copies per wave, K and V each: 16 rows
+    __shared__ __align__(1024) Lds<D> lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h2 = lane >> 5, col = lane & 31;
+
+    const int64_t w = xcd_range(blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0) shared[w].parts = 0;
+    const int64_t head = Line<kRows>::per_head(a), total = head * a.G;
+    if (total <= 0) return;
+    const Cuts cuts(total, (int64_t)kLeast * kKeys * a.group, (int)gridDim.x);
+    if (w >= cuts.workers) return;
+    Place<kRows> at;
+    int64_t x1 = total;
+    if (w + 1 < cuts.workers) {
+        const int64_t x = cuts.at(w + 1);
+        at.find(a, head, x);
+        x1 = at.snap(x);
+    }
+    int64_t x0 = cuts.at(w);
+    at.find(a, head, x0);
+    x0 = w > 0 ? at.snap(x0) : 0;
+    if (x0 >= x1) return;
+    if (x0 >= at.end && !at.next(a)) return;
+
+    // Within the 16 rows that this wave copies of a block: bytes of a row from the first.
+    const int cp_row = lane / SEGS, cp_slot = lane % SEGS;
+    const int64_t k_row = PAGED ? D * 2 : a.k_stride * 2, v_row = PAGED ? D * 2 : a.v_stride * 2;
+    uint32_t k_at[COPIES], v_at[COPIES];
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) {
+        const int r = c * RPT + cp_row, row = 16 * wave + r;
+        k_at[c] = (uint32_t)(r * k_row) + 16 * (cp_slot ^ swz_k<D>(row));
+        v_at[c] = (uint32_t)(r * v_row) + 16 * (cp_slot ^ swz_v<D>(row));
+    }
+    // LDS offsets (of buffer 0): K row `col` (and 32 further), segment 2 t + h2 of
+    // step t; V: lane i of a 16-lane group supplies row i / 4 of four keys, 4
+    // columns from 4 (i % 4) of the group's 16, and gets column i of the four
+    // rows; a step of 16 keys is 16 rows further (the same swizzle).
+    const uint8_t *k_rd[DK], *v_rd[DB];
+#pragma unroll
+    for (int t = 0; t < DK; ++t)
+        k_rd[t] = lds.k[0] + col * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(col));
+    {
+        const int i = lane & 15, row = 4 * h2 + (i >> 2);
+        const int sub = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);     // segment of a 32-wide block
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            v_rd[d] = lds.v[0] + row * (D * 2) + 16 * ((4 * d + sub) ^ swz_v<D>(row)) + 8 * (lane & 1);
+    }
+    const float scale_log2 = a.scale_log2;
+
+    for (;; ) {
+        // ---- one tile, or the part of it that this piece of the line has
+        const int first = at.block_at(x0), last = at.block_at(x1);
+        const bool whole = x0 <= at.begin && x1 >= at.end;
+        const int64_t row0 = at.t * kRows, rows_left = (int64_t)at.s.nq * a.group - row0;
+        if (rows_left <= 0) return;                // (lengths that changed under the call)
+        const int rows = rows_left < kRows ? (int)rows_left : kRows;
+        const int tok0 = (int)(row0 / a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
+        const int nk = at.s.nk, see0 = a.causal ? nk - at.s.nq + 1 : nk;
+        // keys that row i of the tile sees
+        auto limit_of = [&](int i) {
+            const int n = see0 + (a.causal ? tok0 + (rem0 + i) / a.group : 0);
+            return n < 0 ? 0 : n < nk ? n : nk;
+        };
+        const int mine = 32 * wave + col;
+        const bool active = 32 * wave < rows;      // uniform over the wave
+        const int row = mine < rows ? mine : rows - 1;   // rows past the last: never stored
+        const int limit = limit_of(row);
+        const int low = __builtin_amdgcn_readfirstlane(limit_of(active ? 32 * wave : rows - 1));
+        const int high = __builtin_amdgcn_readfirstlane(limit_of(32 * wave + 31 < rows ? 32 * wave + 31 : rows - 1));
+        const int tok = tok0 + (rem0 + row) / a.group, sub = (rem0 + row) % a.group;
+
+        const uint8_t *kb, *vb;
+        int pages = -1;                            // lane l: page of block i0 + l / 4, rows 16 (l % 4) on
+        uint32_t bad = 0, bad_next = 0;            // 16-row parts of a block without a page
+        uint64_t bad16 = 0;
+        if (PAGED) {
+            kb = reinterpret_cast<const uint8_t *>(a.k);
+            vb = reinterpret_cast<const uint8_t *>(a.v);
+        } else {
+            kb = reinterpret_cast<const uint8_t *>(a.k + at.s.k0 * a.k_stride + (int64_t)at.g * D);
+            vb = reinterpret_cast<const uint8_t *>(a.v + at.s.k0 * a.v_stride + (int64_t)at.g * D);
+        }
+        const int32_t *table = PAGED ? a.tables + (int64_t)at.b * a.width : nullptr;
+        auto read_pages = [&](int i0) {            // of 16 blocks
+            const int n = i0 * kKeys + 16 * lane;
+            int p = -1;
+            if (n < nk) p = table[n >> a.page_shift];
+            const bool good = p >= 0 && p < a.pages;
+            pages = good ? p : -1;
+            bad16 = __ballot(!good && n < nk);
+        };
+        // Rows at or past the sequence's keys, and those without a page, are not read: K is left
+        // as it is (its scores are masked, whatever they are), V is zero (the weights are
+        // zero, and zero times what is not finite would be NaN).
+        auto issue = [&](int i, auto buffer) {
+            constexpr int BUF = decltype(buffer)::value;
+            const int n0 = i * kKeys + 16 * wave;
+            int left = nk - n0;
+            const uint8_t *k0, *v0;
+            if (PAGED) {
+                if ((i & 15) == 0 || i == first) read_pages(i & ~15);
+                const int page = __builtin_amdgcn_readlane(pages, 4 * (i & 15) + wave);
+                bad_next = (uint32_t)(bad16 >> (4 * (i & 15))) & 15u;
+                if (page < 0) left = 0;
+                const int64_t r = ((((int64_t)page * a.G + at.g) << a.page_shift) +
+                                   (n0 & ((1 << a.page_shift) - 1))) * (D * 2);
+                k0 = kb + r;
+                v0 = vb + r;
+            } else {
+                k0 = kb + n0 * k_row;
+                v0 = vb + n0 * v_row;
+            }
+            uint8_t *kd = lds.k[BUF] + wave * COPIES * 1024, *vd = lds.v[BUF] + wave * COPIES * 1024;
+            if (__builtin_expect(left >= 16, 1)) {
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) {
+                    copy16_to_lds(k0 + k_at[c], kd + c * 1024);
+                    copy16_to_lds(v0 + v_at[c], vd + c * 1024);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) {
+                    if (c * RPT + cp_row < left) {
+                        copy16_to_lds(k0 + k_at[c], kd + c * 1024);
+                        copy16_to_lds(v0 + v_at[c], vd + c * 1024);
+                    } else {
+                        *reinterpret_cast<u32x4 *>(vd + c * 1024 + lane * 16) = u32x4{};
+                    }
+                }
+            }
+        };
+
+        u32x4 qf[DK];
+        {
+            const uint16_t *p = a.q + (int64_t)(at.s.q0 + tok) * a.q_stride +
+                                (int64_t)(at.g * a.group + sub) * D + 8 * h2;
+#pragma unroll
+            for (int s = 0; s < DK; ++s) qf[s] = *reinterpret_cast<const u32x4 *>(p + 16 * s);
+            // A row with a value that is not finite becomes a row of NaN: scores of minus
+            // infinity alone would look like keys that it does not see.
+            bool odd = false;
+#pragma unroll
+            for (int s = 0; s < DK; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    odd |= (qf[s][j] & 0x7F80u) == 0x7F80u || (qf[s][j] & 0x7F800000u) == 0x7F800000u;
+            const uint64_t rows_odd = __ballot(odd);
+            if (rows_odd && ((rows_odd >> col | rows_odd >> (col + 32)) & 1))
+#pragma unroll
+                for (int s = 0; s < DK; ++s) qf[s] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+        }
+
+        f32x16 o[DB];
+        float m, l;
+        // A v that is not finite, of a key that only some rows of a block see, would reach the
+        // others as zero times it.  That shows as a result that is not finite, and the part is
+        // gone over once more with such values taken out of the blocks that have a mask, and a
+        // NaN put where a row gives one of them a weight.
+        for (bool careful = false;; careful = true) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+            m = -__builtin_inff();
+            l = 0.0f;
+            bool masked = false;
+            auto block = [&](int i, auto buffer) {
+                constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
+                const int n0 = i * kKeys;
+                wait_loads<0>();
+                wave_barrier_all();
+                bad = bad_next;
+                if (i + 1 < last) issue(i + 1, std::integral_constant<int, 1 - BUF>());
+                if (!active || n0 >= high) return;
+                f32x16 s[2] = {f32x16{}, f32x16{}};
+                {
+                    // fragments two steps ahead of the products that use them
+                    u32x4 kf[3][2];
+                    auto load = [&](int t) {
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+                            kf[t % 3][kk] = *reinterpret_cast<const u32x4 *>(k_rd[t] + AT + 32 * kk * (D * 2));
+                    };
+                    load(0);
+                    load(1);
+#pragma unroll
+                    for (int t = 0; t < DK; ++t) {
+                        if (t + 2 < DK) load(t + 2);
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) s[kk] = mfma_bf16_32x32x16(kf[t % 3][kk], qf[t], s[kk]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                // V fragments of a step of 16 keys (kk, t): keys 0 .. 3 and 8 .. 11 past
+                // 4 h2, every 32-wide block of columns
+                u32x4 vf[2][DB];
+                auto load_v = [&](int st) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const u32x2 y = read_transposed(v_rd[d] + AT + (16 * st + 8 * u) * (D * 2));
+                            vf[st & 1][d][2 * u] = y.x;
+                            vf[st & 1][d][2 * u + 1] = y.y;
+                        }
+                };
+                load_v(0);
+                __builtin_amdgcn_sched_barrier(0);
+                const bool edge = n0 + kKeys > low || (PAGED && bad != 0);
+                if (edge) {
+                    masked = true;
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int n = n0 + 32 * kk + 8 * (e / 4) + 4 * h2 + e % 4;
+                            if (n >= limit || (PAGED && (bad >> (2 * kk + e / 8) & 1)))
+                                s[kk][e] = -__builtin_inff();
+                        }
+                }
+                float top = s[0][0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+                top = max_both_halves(top);
+                // The running maximum moves only when a score passes it by more than 8
+                // in the exponent of two: the weights stay below 2^8, and most blocks
+                // leave the sums as they are.
+                if (__any((top - m) * scale_log2 > 8.0f)) {
+                    const float m1 = fmaxf(m, top);
+                    const float f = m == m1 ? 1.0f : __builtin_amdgcn_exp2f((m - m1) * scale_log2);
+                    m = m1;
+                    l *= f;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[d][e] *= f;
+                }
+                // A weight's exponent is s c - fl(m c), c = scale log2 e, in one operation: off
+                // by the rounding of m c, which all keys of a row share: at most 2^-15 up to
+                // |m c| = 2^10.  Past that the difference s - m is taken first (exact where a
+                // weight counts).  A row without a key so far has m = -inf and no offset.
+                float off = m * scale_log2;
+                const bool far = fabsf(off) > 1024.0f;
+                if (__any(far)) {
+                    const float by = far && m > -__builtin_inff() ? m : 0.0f;
+                    off = far ? 0.0f : off;
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[kk][e] -= by;
+                }
+                // [kk][step of 16 keys]: weights, rounded to bf16, the type of the matrix
+                // instruction's operand beside V; the same values go into their sum, so a
+                // row's weights still add up to one.
+                u32x4 p[2][2];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[kk][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kk][e], scale_log2, -off));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            p[kk][t][x] = pack_bf16x2(s[kk][8 * t + 2 * x], s[kk][8 * t + 2 * x + 1]);
+                            l = add_pair(p[kk][t][x], l);
+                        }
+                }
+                if (__builtin_expect(careful && edge, 0)) {
+#pragma unroll 1
+                    for (int st = 0; st < 4; ++st) {
+                        u32x4 ps = p[0][0];
+                        if (st == 1) ps = p[0][1];
+                        if (st == 2) ps = p[1][0];
+                        if (st == 3) ps = p[1][1];
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            u32x4 x, odd;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const u32x2 y = read_transposed(v_rd[d] + AT + (16 * st + 8 * u) * (D * 2));
+                                x[2 * u] = y.x;
+                                x[2 * u + 1] = y.y;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const bool lo = (x[j] & 0x7F80u) == 0x7F80u;
+                                const bool hi = (x[j] & 0x7F800000u) == 0x7F800000u;
+                                odd[j] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
+                                x[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                            }
+                            o[d] = mfma_bf16_32x32x16(x, ps, o[d]);
+                            const f32x16 c = mfma_bf16_32x32x16(odd, ps, f32x16{});
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c[e] > 0.0f) o[d][e] = __builtin_nanf("");
+                        }
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+                    if (st < 3) load_v(st + 1);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[d] = mfma_bf16_32x32x16(vf[st & 1][d], p[st >> 1][st & 1], o[d]);
+                }
+            };
+            if (first < last) issue(first, std::integral_constant<int, 0>());
+            for (int i = first; i < last; i += 2) {
+                block(i, std::integral_constant<int, 0>());
+                if (i + 1 < last) block(i + 1, std::integral_constant<int, 1>());
+            }
+            float z = 0.0f;                        // NaN where something is not finite
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[d][e], 0.0f, z);
+            // (every wave has left the buffers behind this barrier)
+            if (!__syncthreads_or(masked && !careful && z != z)) break;
+        }
+
+        l = sum_both_halves(l);
+        if (!whole) {
+            // unnormalized sums fp32 [slot][row][D], maximum and sum [slot][row][2]
+            const bool begins = x0 <= at.begin;
+            if (mine < rows) {
+                const int64_t r = (2 * w + (begins ? 1 : 0)) * kRows + mine;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<f32x4 *>(part + r * D + 32 * d + 8 * e + 4 * h2) =
+                            f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+                if (h2 == 0) {
+                    stat[2 * r] = m;
+                    stat[2 * r + 1] = l;
+                }
+            }
+            if (begins && threadIdx.x == 0) {
+                // the last worker with a part: the last cut that stays inside the tile
+                int64_t z = cuts.of(at.end - 1);
+                while (z > w + 1 && at.snap(cuts.at(z)) >= at.end) --z;
+                Shared sh;
+                sh.parts = (int)(z - w) + 1;
+                sh.q0 = at.s.q0;
+                sh.g = at.g;
+                sh.rows = rows;
+                sh.row0 = row0;
+                sh.pad = 0;
+                shared[w] = sh;
+            }
+        } else {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            // A lane holds d = 32 db + 8 e + 4 h2 + (0 .. 3) of its row; the swap of
+            // the lane halves gives each eight consecutive ones: 16-byte stores.
+            uint16_t *dst = a.out + ((int64_t)(at.s.q0 + tok) * a.H + at.g * a.group + sub) * D;
+            const bool in = mine < rows;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    u32x2 x[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[u] = u32x2{pack_bf16x2(o[d][4 * (e + u)] * inv, o[d][4 * (e + u) + 1] * inv),
+                                     pack_bf16x2(o[d][4 * (e + u) + 2] * inv, o[d][4 * (e + u) + 3] * inv)};
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(x[0].x, x[1].x, false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(x[0].y, x[1].y, false, false);
+                    if (in)
+                        *reinterpret_cast<u32x4 *>(dst + 32 * d + 8 * (e + h2)) =
+                            u32x4{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+                }
+        }
+        if (x1 <= at.end || !at.next(a)) return;
+    }
+}
+
+// Joins the parts of the shared tile that begins in worker blockIdx.x's piece: the
+// largest maximum, weights 2^(m_i - m) on sums and results.  D / 4 lanes per row,
+// whose first lanes hold one part's maximum and sum each (D / 4 >= 16 parts at a
+// time), so that the loads of all parts are in flight together.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+join_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+            const float *__restrict__ stat) {
+    constexpr int LANES = D / 4;
+    const int64_t w = blockIdx.x;
+    const Shared sh = shared[w];
+    const int r = blockIdx.y * (256 / LANES) + threadIdx.x / LANES;
+    const int c = threadIdx.x % LANES;
+    if (sh.parts == 0 || r >= sh.rows) return;     // whole groups of LANES
+    auto slot = [&](int i) { return (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R + r; };
+    float m = -__builtin_inff(), l = 0.0f;
+    f32x4 o = {};
+    for (int i0 = 0; i0 < sh.parts; i0 += LANES) {
+        const int mine = i0 + c;
+        f32x2 s = {-__builtin_inff(), 0.0f};
+        if (mine < sh.parts) s = *reinterpret_cast<const f32x2 *>(stat + 2 * slot(mine));
+        float top = s.x;
+#pragma unroll
+        for (int d = LANES / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+        const float m1 = fmaxf(m, top);
+        // No maximum yet: parts without a key, whose sums are zero, or the NaN sums of a
+        // query that is not finite, which have to stay.
+        const bool none = m1 == -__builtin_inff();
+        const float f = none ? 1.0f : __builtin_amdgcn_exp2f((m - m1) * a.scale_log2);
+        const float e = none ? 1.0f : __builtin_amdgcn_exp2f((s.x - m1) * a.scale_log2);
+        m = m1;
+        l = l * f + e * s.y;                       // this lane's parts; summed below
+        o *= f;
+        const int n = sh.parts - i0 < LANES ? sh.parts - i0 : LANES;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+            o += __shfl(e, (threadIdx.x & 63) - c + i) *
+                 *reinterpret_cast<const f32x4 *>(part + slot(i0 + i) * D + 4 * c);
+    }
+#pragma unroll
+    for (int d = LANES / 2; d >= 1; d >>= 1) l += __shfl_xor(l, d);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t row = sh.row0 + r, tok = row / a.group;
+    *reinterpret_cast<u32x2 *>(a.out + ((sh.q0 + tok) * a.H + sh.g * a.group + (row - tok * a.group)) * D +
+                               4 * c) =
+        u32x2{pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)};
+}
+
+// Workers: as many workgroups as the compute units hold at once (two each, four at D =
+// 64), or fewer where even the most keys that the shape allows make fewer pieces.  256
+// is the whole card's compute units, not the current device's: the workspace's size
+// follows from it, and has to be the same wherever it is asked for.
+template <int D, int R>
+int workers(const SpanArgs &a) {
+    const int64_t most = D == 64 ? 1024 : 512;
+    const int64_t rows = a.T * a.group, tiles = rows / R + (a.B < a.T ? a.B : a.T);
+    const int64_t blocks = (a.Tk + kKeys - 1) / kKeys + kTileCost / kKeys;
+    const double pieces = (double)tiles * a.G * (double)blocks / kLeast + 1;
+    return pieces < (double)most ? (int)pieces : (int)most;
+}
+
+template <int D, int R>
+size_t bytes(const SpanArgs &a) {
+    const int n = workers<D, R>(a);
+    return header_bytes(n) + (size_t)n * 2 * R * (D + 2) * 4;
+}
+
+template <int D, bool PAGED>
+hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
+    const int n = workers<D, kRows>(a);
+    Shared *shared = static_cast<Shared *>(ws);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + header_bytes(n));
+    float *stat = part + (size_t)n * 2 * kRows * D;
+    span_attention_kernel<D, PAGED><<<n, 256, 0, stream>>>(a, shared, part, stat);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || n == 1) return e;
+    constexpr int per = 256 / (D / 4);
+    join_kernel<D, kRows><<<dim3(n, kRows / per), 256, 0, stream>>>(a, shared, part, stat);
+    return hipGetLastError();
+}
+
+}  // namespace span
+
+size_t span_workspace(const SpanArgs &a) {
+    return a.D == 64 ? span::bytes<64, span::kRows>(a) : span::bytes<128, span::kRows>(a);
+}
+
+hipError_t launch_span_attention(const SpanArgs &a, void *ws, hipStream_t stream) {
+    if (a.kv_len)
+        return a.D == 64 ? span::launch<64, true>(a, ws, stream) : span::launch<128, true>(a, ws, stream);
+    return a.D == 64 ? span::launch<64, false>(a, ws, stream) : span::launch<128, false>(a, ws, stream);
+}
+
+}  // namespace svdq

@@ -1,4 +1,4 @@
-// svdq_wave.h -- device helpers of the 8-bit GEMM and the attention kernels
+// svdq_wave.h -- device helpers of the 8-bit GEMM, rotary and attention kernels
 // (internal; not part of the ABI).
 #pragma once
 
@@ -31,6 +31,19 @@ template <int n>
 __device__ __forceinline__ void wait_loads() {
     static_assert(n >= 0 && n < 64, "vmcnt has six bits");
     __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4));
+}
+
+// Sum over the LPH (8 or 16) consecutive lanes that share a head, every lane
+// getting it: the quad, then its mirror in 8 lanes, then in 16.
+template <int LPH>
+__device__ __forceinline__ float head_sum(float x) {
+    auto add = [&](int moved) { x += __int_as_float(moved); };
+    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, true));   // 7 - lane
+    if (LPH == 16)
+        add(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, true));   // 15 - lane
+    return x;
 }
 
 // GELU, erf form, with one hardware exponential and no reciprocal:

@@ -1,0 +1,372 @@
+"""Attention of packed sequences and over a paged cache against 64-bit plain forms.
+
+Outputs.  With p the exact weights and w = sum p |v|:
+- a score's fp32 sum of D exact products is off by at most (D + 8) 2^-23 scale sum |q k| =: d
+  (the + 8: the product with the scale and the maximum, and the exponent's own rounding), so a
+  weight by a factor within 1 +- d (1 + small), and the normalized one within 1 +- 2 d;
+- each weight is rounded to bf16 for the second product: 2^-8 of it;
+- fp32 sums over n keys of weights and of weighted values: 2 n 2^-23 of w;
+- 2^-12 for the exponential, the reciprocal, a change of the running maximum, the join of
+  parts, and products of the terms above; one rounding of the result to bf16: 2^-8 of it.
+"""
+import numpy as np
+import pytest
+import torch
+
+import bit_diffusion_transformer_amd as bdt
+from tests.helpers import DEV
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def starts_of(lens):
+    return [0] + np.cumsum(lens).tolist()
+
+
+def sequence_64(q, k, v, scale, causal, dead=None):
+    """(out, tolerance) fp64 [n, H, D] of one sequence: q [n, H, D], k, v [m, G, D]; dead [m]:
+    keys that no row sees."""
+    n, H, D = q.shape
+    m, G = k.shape[:2]
+    out = torch.zeros(n, H, D, dtype=torch.float64, device=q.device)
+    tol = torch.zeros_like(out)
+    if n == 0 or m == 0:
+        return out, tol
+    key = torch.arange(m, device=q.device)
+    row = torch.arange(n, device=q.device)
+    sees = key[None, :] <= row[:, None] + (m - n) if causal else torch.ones(n, m, dtype=torch.bool,
+                                                                            device=q.device)
+    if dead is not None:
+        sees = sees & ~dead[None, :]
+    any_key = sees.any(1)
+    used = sees.any(0)
+    for h in range(H):
+        qd, kd, vd = q[:, h].double(), k[:, h // (H // G)].double(), v[:, h // (H // G)].double()
+        kd = torch.where(used[:, None], kd, 0.0)
+        vd = torch.where(used[:, None], vd, 0.0)
+        s = scale * (qd @ kd.t())
+        s = s.masked_fill(~sees, -float("inf"))
+        p = torch.softmax(torch.where(any_key[:, None], s, 0.0), dim=1)
+        p = torch.where(any_key[:, None] & sees, p, 0.0)
+        o, w = p @ vd, p @ vd.abs()
+        d = (D + 8) * 2.0 ** -23 * scale * (qd.abs() @ kd.abs().t()).amax(1, keepdim=True)
+        out[:, h] = o
+        tol[:, h] = 2.0 ** -8 * o.abs() + w * (2 * d + 2.0 ** -8 + 2 * m * 2.0 ** -23 + 2.0 ** -12)
+    return out, tol
+
+
+def check(out, ref, tol, what):
+    err = (out.double() - ref).abs()
+    assert bool(torch.isfinite(out.float()).all()), "%s: not finite" % what
+    assert bool((err <= tol + 1e-30).all()), "%s: worst %.3g of the bound" % (
+        what, float((err / (tol + 1e-30)).max()))
+
+
+def normal(seed, *shape, gain=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (gain * torch.randn(shape, generator=g, device=DEV)).to(BF)
+
+
+# ------------------------------------------------------------------ packed
+
+PACKED = [
+    # H, G, D, lens
+    (1, 1, 128, [1]), (1, 1, 64, [1]), (2, 1, 64, [63]), (3, 3, 128, [64]), (4, 1, 128, [65]),
+    (5, 5, 64, [2, 1, 3]), (6, 2, 128, [127, 0, 128, 129]), (8, 8, 64, [300, 77, 1]),
+    (7, 1, 128, [100, 1, 257]), (12, 4, 64, [511, 0, 0, 513]), (16, 1, 128, [33, 34]),
+    (64, 1, 64, [9, 40]), (24, 8, 128, [640, 1000]), (10, 2, 64, [1500]), (4, 2, 128, [3001]),
+    (3, 1, 128, [200, 1] * 40), (2, 2, 64, [5] * 130 + [700]), (8, 2, 128, [0, 0, 2048, 0]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,G,D,lens", PACKED)
+def test_packed_attention(H, G, D, lens, causal):
+    T = sum(lens)
+    q, k, v = normal(1, T, H, D, gain=1.5), normal(2, T, G, D), normal(3, T, G, D)
+    at = starts_of(lens)
+    out = bdt.packed_attention(q, k, v, ints(at), causal=causal)
+    assert out.shape == (T, H, D)
+    for a, b in zip(at[:-1], at[1:]):
+        ref, tol = sequence_64(q[a:b], k[a:b], v[a:b], D ** -0.5, causal)
+        check(out[a:b], ref, tol, "rows %d .. %d" % (a, b))
+    assert torch.equal(bdt.packed_attention(q, k, v, ints(at), causal=causal), out)
+
+
+@pytest.mark.parametrize("H,G,D,lens,keys", [
+    (2, 1, 128, [3, 1, 70], [500, 0, 70]), (4, 4, 64, [1], [4000]), (6, 2, 128, [130, 5], [64, 3000]),
+    (8, 2, 128, [1, 1, 1, 200], [1, 0, 2000, 199]), (2, 2, 64, [300], [10]),
+    (12, 12, 128, [1560, 77], [400, 333]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_keys_of_their_own(H, G, D, lens, keys, causal):
+    """Fewer keys than rows: with causal the first rows see none."""
+    T, Tk = sum(lens), sum(keys)
+    q, k, v = normal(4, T, H, D), normal(5, Tk, G, D), normal(6, Tk, G, D)
+    qa, ka = starts_of(lens), starts_of(keys)
+    out = bdt.packed_attention(q, k, v, ints(qa), ints(ka), causal=causal, scale=0.2)
+    for i in range(len(lens)):
+        x, y = slice(qa[i], qa[i + 1]), slice(ka[i], ka[i + 1])
+        ref, tol = sequence_64(q[x], k[y], v[y], 0.2, causal)
+        check(out[x], ref, tol, "sequence %d" % i)
+        if causal and lens[i] > keys[i]:
+            assert bool((out[x][:lens[i] - keys[i]] == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_parts_of_a_projection(D):
+    """q, k and v as columns of one projection, and rows behind the last sequence."""
+    H, G, lens = 6, 2, [70, 0, 333]
+    T = sum(lens) + 9
+    qkv = normal(7, T, (H + 2 * G) * D)
+    q, k, v = (x.view(T, -1, D) for x in qkv.split([H * D, G * D, G * D], dim=1))
+    assert not q.is_contiguous()
+    buf = torch.full((T, H, D), -777.0, dtype=BF, device=DEV)
+    out = bdt.packed_attention(q, k, v, ints(starts_of(lens)), out=buf)
+    assert out is buf and bool((buf[-9:] == -777).all())
+    want = bdt.packed_attention(q.contiguous(), k.contiguous(), v.contiguous(), ints(starts_of(lens)))
+    assert torch.equal(out[:-9], want[:-9])
+    bits = bdt.packed_attention(q.view(torch.int16), k.view(torch.int16), v, ints(starts_of(lens)))
+    assert torch.equal(bits[:-9], want[:-9])
+
+
+# ------------------------------------------------------------------ paged
+
+def paged_inputs(H, G, D, page, new, lens, seed, spare=3, gain=1.0):
+    """(q, k_cache, v_cache, tables, dense k, dense v): pages in a mixed order; what no request
+    holds is NaN or infinite."""
+    T, each = sum(new), [-(-n // page) for n in lens]
+    pages, width = sum(each) + spare, max(each + [0]) + 2
+    q = normal(seed, T, H, D, gain=gain)
+    kc = torch.full((pages, G, page, D), float("nan"), dtype=BF, device=DEV)
+    vc = torch.full((pages, G, page, D), float("inf"), dtype=BF, device=DEV)
+    vc[..., ::2] = float("nan")
+    order = np.random.default_rng(seed).permutation(pages)
+    tables = np.full((len(new), width), 7 * pages + 11, np.int64)
+    tables[:, 1::2] = -5
+    ks, vs, at = [], [], 0
+    for b, n in enumerate(lens):
+        k, v = normal(seed + 10 + b, n, G, D), normal(seed + 1000 + b, n, G, D)
+        ks.append(k)
+        vs.append(v)
+        for i in range(each[b]):
+            p = int(order[at])
+            at += 1
+            tables[b, i] = p
+            part = slice(i * page, min((i + 1) * page, n))
+            kc[p, :, :part.stop - part.start] = k[part].transpose(0, 1)
+            vc[p, :, :part.stop - part.start] = v[part].transpose(0, 1)
+    return q, kc, vc, ints(tables.astype(np.int32).tolist()).view(len(new), width), ks, vs
+
+
+PAGED = [
+    # H, G, D, page, new, lens
+    (1, 1, 128, 16, [1], [1]), (1, 1, 64, 16, [1], [17]), (8, 2, 128, 64, [1], [5000]),
+    (32, 8, 128, 16, [1] * 9, [9, 1, 16, 17, 333, 64, 65, 4097, 128]), (4, 4, 64, 32, [1, 1], [0, 100]),
+    (6, 1, 128, 128, [1, 0, 2, 5], [300, 50, 700, 5]), (16, 1, 64, 256, [1, 1, 1], [2000, 256, 257]),
+    (12, 12, 128, 64, [3, 1], [1000, 999]), (28, 4, 64, 32, [1, 1, 130, 1], [90, 300, 800, 31]),
+    (4, 2, 128, 16, [64], [64]), (8, 1, 128, 64, [40, 17], [3000, 17]), (2, 2, 128, 256, [700], [1500]),
+    (5, 5, 64, 16, [129], [3000]), (64, 1, 128, 16, [1, 3], [700, 4]), (3, 1, 128, 64, [1] * 70, list(range(1, 140, 2))),
+    (8, 8, 128, 64, [5, 5], [3, 5]), (24, 24, 64, 64, [1], [20000]), (10, 2, 128, 32, [16, 7], [2222, 4444]),
+    (16, 2, 128, 128, [2, 4, 1], [9000, 31, 12000]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,G,D,page,new,lens", PAGED)
+def test_paged_attention(H, G, D, page, new, lens, causal):
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, new, lens, 20)
+    at, kv = starts_of(new), ints(lens)
+    outs = [bdt.paged_attention(q, kc, vc, tables, ints(at), kv, max_new=most, causal=causal)
+            for most in (max(new), None, 1)]
+    for out in outs:
+        for b in range(len(new)):
+            x = slice(at[b], at[b + 1])
+            ref, tol = sequence_64(q[x], ks[b], vs[b], D ** -0.5, causal)
+            check(out[x], ref, tol, "request %d" % b)
+    assert torch.equal(bdt.paged_attention(q, kc, vc, tables, ints(at), kv, max_new=max(new),
+                                           causal=causal), outs[0])
+
+
+@pytest.mark.parametrize("H,G,new,lens", [(8, 2, [1, 1], [900, 130]), (4, 4, [70, 1], [900, 130]),
+                                          (16, 2, [3, 2], [900, 130])])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_outside_the_cache_hold_no_keys(D, page, H, G, new, lens):
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, new, lens, 3)
+    host = tables.cpu()
+    dead = [torch.zeros(n, dtype=torch.bool, device=DEV) for n in lens]
+    for b, i, entry in ((0, 1, -1), (0, 2, kc.shape[0]), (1, 0, 2 ** 31 - 1), (0, 3, -2 ** 31)):
+        if i * page < lens[b]:
+            host[b, i] = entry
+            dead[b][i * page:(i + 1) * page] = True
+    at = starts_of(new)
+    out = bdt.paged_attention(q, kc, vc, host.to(DEV), ints(at), ints(lens), max_new=max(new))
+    for b in range(2):
+        x = slice(at[b], at[b + 1])
+        ref, tol = sequence_64(q[x], ks[b], vs[b], D ** -0.5, True, dead[b])
+        check(out[x], ref, tol, "request %d" % b)
+    host.fill_(-1)
+    out = bdt.paged_attention(q, kc, vc, host.to(DEV), ints(at), ints(lens), max_new=max(new))
+    assert bool((out == 0).all())
+    none = bdt.paged_attention(q, kc[:0], vc[:0], tables, ints(at), ints(lens), max_new=max(new))
+    assert bool((none == 0).all())
+
+
+def test_lengths_past_the_table_and_starts_out_of_order():
+    """Lengths are clamped to the table's width; starts are clamped, and a sequence that ends
+    before it starts has no rows; rows of no sequence stay."""
+    H, G, D, page = 4, 2, 128, 16
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, [2, 3], [48, 48], 5)
+    full = tables[:, :3].contiguous()
+    want = bdt.paged_attention(q, kc, vc, full, ints([0, 2, 5]), ints([48, 48]))
+    got = bdt.paged_attention(q, kc, vc, full, ints([0, 2, 5]), ints([49, 2 ** 31 - 1]))
+    assert torch.equal(got, want)
+    buf = torch.full_like(q, -777.0)
+    bdt.paged_attention(q, kc, vc, full, ints([-7, 2, 1]), ints([48, -3]), out=buf)
+    assert torch.equal(buf[:2], want[:2]) and bool((buf[2:] == -777).all())
+    buf.fill_(-777.0)
+    bdt.paged_attention(q, kc, vc, full, ints([2, 5, 2 ** 31 - 1]), ints([0, 48]), out=buf)
+    assert bool((buf[:2] == -777).all()) and bool((buf[2:] == 0).all())
+
+
+# ------------------------------------------------------------------ values
+
+@pytest.mark.parametrize("gain", [0.0, 40.0, 4000.0])
+@pytest.mark.parametrize("new,lens", [([1, 1], [3000, 70]), ([300, 2], [2000, 40])])
+def test_extreme_scores(gain, new, lens):
+    H, G, D = 4, 2, 128
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, 64, new, lens, 9, gain=gain)
+    at = starts_of(new)
+    out = bdt.paged_attention(q, kc, vc, tables, ints(at), ints(lens), max_new=max(new))
+    for b in range(2):
+        x = slice(at[b], at[b + 1])
+        ref, tol = sequence_64(q[x], ks[b], vs[b], D ** -0.5, True)
+        check(out[x], ref, tol, "gain %g" % gain)
+
+
+@pytest.mark.parametrize("H,G,D,lens", [(4, 1, 128, [200, 300]), (2, 2, 64, [130, 700]), (8, 2, 128, [10, 20]),
+                                        (1, 1, 128, [3000])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_later_keys_that_are_not_finite_stay_out_of_earlier_rows(H, G, D, lens, bad):
+    T, at = sum(lens), starts_of(lens)
+    q, k, v = normal(1, T, H, D), normal(2, T, G, D), normal(3, T, G, D)
+    clean = bdt.packed_attention(q, k, v, ints(at))
+    n = at[-1] - 5                                   # a late key of the last sequence
+    kb, vb = k.clone(), v.clone()
+    kb[n], vb[n, :, 3] = float("nan"), bad
+    out = bdt.packed_attention(q, kb, vb, ints(at))
+    assert torch.equal(out[:n], clean[:n])
+    assert bool(out[n:].isnan().all())
+    out = bdt.packed_attention(q, k, vb, ints(at))
+    assert torch.equal(out[:n], clean[:n])
+    other = [d for d in range(D) if d != 3]
+    assert torch.equal(out[n:][..., other], clean[n:][..., other])
+    assert not bool(torch.isfinite(out[n:, :, 3]).any())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("new,lens", [([1, 1], [4000, 70]), ([200, 2], [2000, 40])])
+def test_a_query_that_is_not_finite(bad, new, lens):
+    H, G, D = 4, 2, 128
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, 64, new, lens, 9)
+    args = (kc, vc, tables, ints(starts_of(new)), ints(lens))
+    clean = bdt.paged_attention(q, *args, max_new=max(new))
+    q[0, 1, 77] = bad
+    out = bdt.paged_attention(q, *args, max_new=max(new))
+    assert bool(out[0, 1].isnan().all())
+    out[0, 1] = clean[0, 1]
+    assert torch.equal(out, clean)
+
+
+def test_outputs_and_workspace_stay_inside():
+    for H, G, D, new, lens in ((4, 2, 128, [1, 1], [3000, 500]), (6, 2, 64, [150, 3], [1000, 40])):
+        q, kc, vc, tables, _, _ = paged_inputs(H, G, D, 64, new, lens, 2)
+        T, at = sum(new), ints(starts_of(new))
+        s = bdt.PagedShape(T, kc.shape[0], H * D, len(new), H, G, D, 64, tables.shape[1], max(new), 1)
+        need = bdt.svdq_paged_attention_workspace_bytes(s)
+        n = q.numel()
+        buf = torch.full((n + 512,), -777.0, dtype=BF, device=DEV)
+        ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+        bdt.svdq_paged_attention(q, kc, vc, tables, at, ints(lens), s, D ** -0.5, buf[256:256 + n],
+                                 ws[256:], need)
+        assert bool((buf[:256] == -777).all()) and bool((buf[256 + n:] == -777).all())
+        assert bool((ws[:256] == 0xFF).all()) and bool((ws[256 + need:] == 0xFF).all())
+        out = bdt.paged_attention(q, kc, vc, tables, at, ints(lens), max_new=max(new))
+        assert torch.equal(buf[256:256 + n].view_as(out), out)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [90, 1, 40]])
+def test_in_a_graph_and_on_two_streams(new):
+    H, G, D, page = 8, 2, 128, 32
+    lens = [2000, 300, 777]
+    sets = [paged_inputs(H, G, D, page, new, lens, seed)[:4] for seed in (1, 2)]
+    at, kv = ints(starts_of(new)), ints(lens)
+
+    def call(q, kc, vc, t, kv=kv):
+        return bdt.paged_attention(q, kc, vc, t, at, kv, max_new=max(new))
+    want = [call(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(call(*s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    mine = [x.clone() for x in sets[0]]
+    length = kv.clone()
+    with torch.cuda.stream(streams[0]):
+        call(*mine, kv=length)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(*mine, kv=length)
+    for it in range(5):
+        for dst, src in zip(mine, sets[it % 2]):
+            dst.copy_(src)
+        length.copy_(kv if it < 3 else kv // 3)                # lengths read at replay
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = call(*mine, kv=length)
+        assert torch.equal(out, eager), "replay %d" % it
+        if it < 3:
+            assert torch.equal(out, want[it % 2])
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements; the request's pages are its last ones."""
+    G, page, D, n = 8, 256, 128, 700
+    pages = 8300
+    kc = torch.zeros(pages, G, page, D, dtype=BF, device=DEV)
+    assert kc.numel() > 1 << 31
+    vc = torch.zeros_like(kc)
+    k, v = normal(1, n, G, D), normal(2, n, G, D)
+    table = [pages - 1, pages - 3, pages - 2]
+    for i, p in enumerate(table):
+        part = slice(i * page, min((i + 1) * page, n))
+        kc[p, :, :part.stop - part.start] = k[part].transpose(0, 1)
+        vc[p, :, :part.stop - part.start] = v[part].transpose(0, 1)
+    for m in (1, 60):
+        q = normal(3, m, 2 * G, D)
+        out = bdt.paged_attention(q, kc, vc, ints([table]), ints([0, m]), ints([n]), max_new=m)
+        ref, tol = sequence_64(q, k, v, D ** -0.5, True)
+        check(out, ref, tol, "%d rows" % m)
+
+
+def test_empty():
+    q = torch.empty(0, 4, 64, dtype=BF, device=DEV)
+    k = torch.empty(0, 2, 64, dtype=BF, device=DEV)
+    assert bdt.packed_attention(q, k, k, ints([0])).shape == (0, 4, 64)
+    assert bdt.packed_attention(q, k, k, ints([0, 0])).shape == (0, 4, 64)
+    q = normal(1, 3, 4, 64)
+    out = bdt.packed_attention(q, k, k, ints([0, 3]), ints([0, 0]), causal=False)
+    assert bool((out == 0).all())
+    buf = torch.full_like(q, 5.0)
+    assert bool((bdt.packed_attention(q, q, q, ints([0]), out=buf) == 5).all())
