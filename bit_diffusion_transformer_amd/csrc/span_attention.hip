@@ -200,12 +200,13 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         // others as zero times it.  That shows as a result that is not finite, and the part is
         // gone over once more with such values taken out of the blocks that have a mask, and a
         // NaN put where a row gives one of them a weight.
-        for (bool careful = false;; careful = true) {
+        bool masked = false;
+        auto pass = [&](auto mode) {
+            constexpr bool careful = decltype(mode)::value;
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[d] = f32x16{};
             m = -__builtin_inff();
             l = 0.0f;
-            bool masked = false;
             auto block = [&](int i, auto buffer) {
                 constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
                 const int n0 = i * kKeys;
@@ -311,7 +312,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                             l = add_pair(p[kk][t][x], l);
                         }
                 }
-                if (__builtin_expect(careful && edge, 0)) {
+                if (careful && edge) {
 #pragma unroll 1
                     for (int st = 0; st < 4; ++st) {
                         u32x4 ps = p[0][0];
@@ -355,13 +356,17 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 block(i, std::integral_constant<int, 0>());
                 if (i + 1 < last) block(i + 1, std::integral_constant<int, 1>());
             }
-            float z = 0.0f;                        // NaN where something is not finite
+        };
+        pass(std::false_type());
+        float z = 0.0f;                            // NaN where something is not finite
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[d][e], 0.0f, z);
-            // (every wave has left the buffers behind this barrier)
-            if (!__syncthreads_or(masked && !careful && z != z)) break;
+            for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[d][e], 0.0f, z);
+        // (every wave has left the buffers behind these barriers)
+        if (__builtin_expect(__syncthreads_or(masked && z != z), 0)) {
+            pass(std::true_type());
+            __syncthreads();
         }
 
         l = sum_both_halves(l);
