@@ -14,7 +14,7 @@ LIB = os.path.join(PKG, "libsvdq.so")
 SOURCES = ["svdq_api.hip", "quant_down.hip", "w4a4_gemm.hip", "w4a4_gemm_qkv.hip", "w4a4_gemm_mlp.hip",
            "w4a4_mx_gemm.hip", "awq_w4a16.hip", "w4a4_gemm_sums.hip", "w4a4_gemm_ks.hip",
            "attention_api.hip", "qkv_rope.hip", "block_select.hip", "block_attention.hip",
-           "paged_api.hip", "span_attention.hip", "page_tables.hip", "cache_rope.hip",
+           "paged_api.hip", "span_attention.hip", "span_few.hip", "page_tables.hip", "cache_rope.hip",
            "i8_api.hip", "i8_quantize.hip", "i8_gemm.hip", "i8_few.hip"]
 ARCH = "gfx950"
 

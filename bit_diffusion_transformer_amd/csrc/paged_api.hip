@@ -59,11 +59,11 @@ int32_t read_pages(int32_t page, int64_t pages, int64_t width, int &shift) {
     return SVDQ_OK;
 }
 
-// The line of all tiles has to fit 62 bits (span_plan.h), whatever the starts are.
+// The line of all tiles has to fit 52 bits (span_plan.h).
 int32_t check_line(const SpanArgs &a) {
-    const double tiles = ((double)a.T * a.group / 16 + 1) * a.B;
+    const double tiles = (double)a.T * a.group / 16 + a.B;
     const double each = a.group * ((double)a.Tk + 128) + (double)a.T * a.group + 128;
-    if (tiles * each * a.G > 0x1p62)
+    if (tiles * each * a.G > 0x1p52)
         return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%lld rows of %d sequences over %lld keys are too many",
                     (long long)a.T, a.B, (long long)a.Tk);
     return SVDQ_OK;
@@ -132,13 +132,20 @@ int32_t read_scale(float scale, SpanArgs &a) {
     return SVDQ_OK;
 }
 
+// New tokens whose rows fit a wave's tile: their time is that of reading the cache.
+bool few(const SpanArgs &a) { return a.max_new > 0 && (int64_t)a.max_new * a.group <= 32; }
+
+size_t workspace_bytes(const SpanArgs &a) { return few(a) ? span_few_workspace(a) : span_tile_workspace(a); }
+
 int32_t run(const SpanArgs &a, void *workspace, size_t ws_bytes, void *stream) {
-    const size_t need = span_workspace(a);
+    const size_t need = workspace_bytes(a);
     if (ws_bytes < need)
         return fail(SVDQ_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes < %zu needed", ws_bytes, need);
     SVDQ_TRY(need_ptr(workspace, "workspace"));
     SVDQ_TRY(check_device());
-    return hip_status(launch_span_attention(a, workspace, (hipStream_t)stream), "attention launch");
+    hipStream_t s = (hipStream_t)stream;
+    return hip_status(few(a) ? launch_span_few(a, workspace, s) : launch_span_tiles(a, workspace, s),
+                      "attention launch");
 }
 
 }  // namespace
@@ -147,7 +154,7 @@ extern "C" {
 
 size_t svdq_packed_attention_workspace_bytes(const svdq_packed_shape *shape) {
     SpanArgs a;
-    return read_shape(shape, true, a) == SVDQ_OK && !empty(a) ? span_workspace(a) : 0;
+    return read_shape(shape, true, a) == SVDQ_OK && !empty(a) ? workspace_bytes(a) : 0;
 }
 
 int32_t svdq_packed_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
@@ -178,7 +185,7 @@ int32_t svdq_packed_attention(const uint16_t *q, const uint16_t *k, const uint16
 
 size_t svdq_paged_attention_workspace_bytes(const svdq_paged_shape *shape) {
     SpanArgs a;
-    return read_shape(shape, a) == SVDQ_OK && !empty(a) ? span_workspace(a) : 0;
+    return read_shape(shape, a) == SVDQ_OK && !empty(a) ? workspace_bytes(a) : 0;
 }
 
 int32_t svdq_paged_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,

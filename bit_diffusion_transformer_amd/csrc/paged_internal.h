@@ -25,8 +25,11 @@ struct SpanArgs {
     float scale_log2;                    // scale log2(e)
 };
 
-size_t span_workspace(const SpanArgs &a);
-hipError_t launch_span_attention(const SpanArgs &a, void *ws, hipStream_t stream);
+// Tiles of 128 rows; paged with at most 32 rows of a request and key head: a wave each.
+size_t span_tile_workspace(const SpanArgs &a);
+hipError_t launch_span_tiles(const SpanArgs &a, void *ws, hipStream_t stream);
+size_t span_few_workspace(const SpanArgs &a);
+hipError_t launch_span_few(const SpanArgs &a, void *ws, hipStream_t stream);
 
 struct TableArgs {
     const int32_t *cached, *added, *free_pages;

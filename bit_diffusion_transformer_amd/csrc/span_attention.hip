@@ -26,12 +26,8 @@ struct Lds {
     static constexpr int TILE = kKeys * D * 2;     // bytes of a K or V block
     uint8_t k[2][TILE];
     uint8_t v[2][TILE];
+    Seq seqs[4][64];                               // a wave each: they are not in step
 };
-
-// The workspace: shared tiles' headers (one a worker), then partial results, two
-// slots a worker: 2 w + 1 for the tile that begins in its piece and ends
-// outside, 2 w for the one that began before.
-__host__ __device__ inline size_t header_bytes(int workers) { return align256((size_t)workers * sizeof(Shared)); }
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(256, D == 64 ? 4 : 2)
@@ -45,24 +41,11 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5, col = lane & 31;
 
-    const int64_t w = xcd_range(blockIdx.x, gridDim.x);
+    const int w = (int)xcd_range(blockIdx.x, gridDim.x);
     if (threadIdx.x == 0) shared[w].parts = 0;
-    const int64_t head = Line<kRows>::per_head(a), total = head * a.G;
-    if (total <= 0) return;
-    const Cuts cuts(total, (int64_t)kLeast * kKeys * a.group, (int)gridDim.x);
-    if (w >= cuts.workers) return;
-    Place<kRows> at;
-    int64_t x1 = total;
-    if (w + 1 < cuts.workers) {
-        const int64_t x = cuts.at(w + 1);
-        at.find(a, head, x);
-        x1 = at.snap(x);
-    }
-    int64_t x0 = cuts.at(w);
-    at.find(a, head, x0);
-    x0 = w > 0 ? at.snap(x0) : 0;
-    if (x0 >= x1) return;
-    if (x0 >= at.end && !at.next(a)) return;
+    Piece<kRows> piece;
+    if (!piece.open(a, lds.seqs[wave], w, (int)gridDim.x)) return;
+    Place<kRows> &at = piece.at;
 
     // Within the 16 rows that this wave copies of a block: bytes of a row from the first.
     const int cp_row = lane / SEGS, cp_slot = lane % SEGS;
@@ -89,16 +72,16 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         for (int d = 0; d < DB; ++d)
             v_rd[d] = lds.v[0] + row * (D * 2) + 16 * ((4 * d + sub) ^ swz_v<D>(row)) + 8 * (lane & 1);
     }
+    const uint32_t lds_k = lds_address(lds.k) + wave * COPIES * 1024, lds_v = lds_address(lds.v) + wave * COPIES * 1024;
     const float scale_log2 = a.scale_log2;
 
     for (;; ) {
         // ---- one tile, or the part of it that this piece of the line has
-        const int first = at.block_at(x0), last = at.block_at(x1);
-        const bool whole = x0 <= at.begin && x1 >= at.end;
+        const int first = at.block_at(piece.x0), last = at.block_at(piece.x1);
         const int64_t row0 = at.t * kRows, rows_left = (int64_t)at.s.nq * a.group - row0;
         if (rows_left <= 0) return;                // (lengths that changed under the call)
         const int rows = rows_left < kRows ? (int)rows_left : kRows;
-        const int tok0 = (int)(row0 / a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
+        const int tok0 = (int)quotient(row0, a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
         const int nk = at.s.nk, see0 = a.causal ? nk - at.s.nq + 1 : nk;
         // keys that row i of the tile sees
         auto limit_of = [&](int i) {
@@ -154,21 +137,20 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 k0 = kb + n0 * k_row;
                 v0 = vb + n0 * v_row;
             }
-            uint8_t *kd = lds.k[BUF] + wave * COPIES * 1024, *vd = lds.v[BUF] + wave * COPIES * 1024;
+            const uint32_t kd = lds_k + BUF * Lds<D>::TILE, vd = lds_v + BUF * Lds<D>::TILE;
+            k0 = uniform_pointer(k0);
+            v0 = uniform_pointer(v0);
             if (__builtin_expect(left >= 16, 1)) {
-#pragma unroll
-                for (int c = 0; c < COPIES; ++c) {
-                    copy16_to_lds(k0 + k_at[c], kd + c * 1024);
-                    copy16_to_lds(v0 + v_at[c], vd + c * 1024);
-                }
+                copies_in_flight(k0, k_at, kd);
+                copies_in_flight(v0, v_at, vd);
             } else {
 #pragma unroll
                 for (int c = 0; c < COPIES; ++c) {
                     if (c * RPT + cp_row < left) {
-                        copy16_to_lds(k0 + k_at[c], kd + c * 1024);
-                        copy16_to_lds(v0 + v_at[c], vd + c * 1024);
+                        copy_in_flight(k0, k_at[c], kd + c * 1024);
+                        copy_in_flight(v0, v_at[c], vd + c * 1024);
                     } else {
-                        *reinterpret_cast<u32x4 *>(vd + c * 1024 + lane * 16) = u32x4{};
+                        *reinterpret_cast<u32x4 *>(lds.v[BUF] + (wave * COPIES + c) * 1024 + lane * 16) = u32x4{};
                     }
                 }
             }
@@ -370,11 +352,11 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         }
 
         l = sum_both_halves(l);
-        if (!whole) {
+        if (!piece.whole()) {
             // unnormalized sums fp32 [slot][row][D], maximum and sum [slot][row][2]
-            const bool begins = x0 <= at.begin;
+            const bool begins = piece.begins();
             if (mine < rows) {
-                const int64_t r = (2 * w + (begins ? 1 : 0)) * kRows + mine;
+                const int64_t r = (int64_t)(2 * w + (begins ? 1 : 0)) * kRows + mine;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -386,12 +368,9 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                     stat[2 * r + 1] = l;
                 }
             }
-            if (begins && threadIdx.x == 0) {
-                // the last worker with a part: the last cut that stays inside the tile
-                int64_t z = cuts.of(at.end - 1);
-                while (z > w + 1 && at.snap(cuts.at(z)) >= at.end) --z;
+            if (begins && threadIdx.x < 64) {        // (all lanes write the same)
                 Shared sh;
-                sh.parts = (int)(z - w) + 1;
+                sh.parts = piece.parts();
                 sh.q0 = at.s.q0;
                 sh.g = at.g;
                 sh.rows = rows;
@@ -421,98 +400,67 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                             u32x4{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
                 }
         }
-        if (x1 <= at.end || !at.next(a)) return;
+        if (!piece.next(a)) return;
     }
 }
 
 // Joins the parts of the shared tile that begins in worker blockIdx.x's piece: the
 // largest maximum, weights 2^(m_i - m) on sums and results.  D / 4 lanes per row,
-// whose first lanes hold one part's maximum and sum each (D / 4 >= 16 parts at a
-// time), so that the loads of all parts are in flight together.
-template <int D, int R>
+// four rows of a thread at once: a tile of prompts has two or three parts, and
+// its 128 rows are what has to be in flight.
+template <int D>
 __global__ void __launch_bounds__(256)
-join_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
-            const float *__restrict__ stat) {
-    constexpr int LANES = D / 4;
+join_rows_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+                 const float *__restrict__ stat) {
+    constexpr int LANES = D / 4, STEP = 256 / LANES;
     const int64_t w = blockIdx.x;
     const Shared sh = shared[w];
-    const int r = blockIdx.y * (256 / LANES) + threadIdx.x / LANES;
-    const int c = threadIdx.x % LANES;
-    if (sh.parts == 0 || r >= sh.rows) return;     // whole groups of LANES
-    auto slot = [&](int i) { return (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R + r; };
-    float m = -__builtin_inff(), l = 0.0f;
-    f32x4 o = {};
-    for (int i0 = 0; i0 < sh.parts; i0 += LANES) {
-        const int mine = i0 + c;
-        f32x2 s = {-__builtin_inff(), 0.0f};
-        if (mine < sh.parts) s = *reinterpret_cast<const f32x2 *>(stat + 2 * slot(mine));
-        float top = s.x;
+    const int r0 = blockIdx.y * (4 * STEP) + threadIdx.x / LANES, c = threadIdx.x % LANES;
+    if (sh.parts == 0 || r0 >= sh.rows) return;
+    Joined j[4] = {Joined::none(), Joined::none(), Joined::none(), Joined::none()};
+#pragma unroll 2
+    for (int i = 0; i < sh.parts; ++i) {
+        const int64_t slot = (i == 0 ? 2 * w + 1 : 2 * (w + i)) * kRows;
+        f32x2 s[4];
+        f32x4 o[4];
 #pragma unroll
-        for (int d = LANES / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        const float m1 = fmaxf(m, top);
-        // No maximum yet: parts without a key, whose sums are zero, or the NaN sums of a
-        // query that is not finite, which have to stay.
-        const bool none = m1 == -__builtin_inff();
-        const float f = none ? 1.0f : __builtin_amdgcn_exp2f((m - m1) * a.scale_log2);
-        const float e = none ? 1.0f : __builtin_amdgcn_exp2f((s.x - m1) * a.scale_log2);
-        m = m1;
-        l = l * f + e * s.y;                       // this lane's parts; summed below
-        o *= f;
-        const int n = sh.parts - i0 < LANES ? sh.parts - i0 : LANES;
-#pragma unroll 8
-        for (int i = 0; i < n; ++i)
-            o += __shfl(e, (threadIdx.x & 63) - c + i) *
-                 *reinterpret_cast<const f32x4 *>(part + slot(i0 + i) * D + 4 * c);
+        for (int u = 0; u < 4; ++u) {
+            const int64_t r = slot + (r0 + u * STEP < sh.rows ? r0 + u * STEP : r0);
+            s[u] = *reinterpret_cast<const f32x2 *>(stat + 2 * r);
+            o[u] = *reinterpret_cast<const f32x4 *>(part + r * D + 4 * c);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) j[u].add(s[u].x, s[u].y, o[u], a.scale_log2);
     }
 #pragma unroll
-    for (int d = LANES / 2; d >= 1; d >>= 1) l += __shfl_xor(l, d);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int64_t row = sh.row0 + r, tok = row / a.group;
-    *reinterpret_cast<u32x2 *>(a.out + ((sh.q0 + tok) * a.H + sh.g * a.group + (row - tok * a.group)) * D +
-                               4 * c) =
-        u32x2{pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)};
+    for (int u = 0; u < 4; ++u)
+        if (r0 + u * STEP < sh.rows) store_joined<D>(a, sh, r0 + u * STEP, c, j[u]);
 }
 
 // Workers: as many workgroups as the compute units hold at once (two each, four at D =
-// 64), or fewer where even the most keys that the shape allows make fewer pieces.  256
-// is the whole card's compute units, not the current device's: the workspace's size
-// follows from it, and has to be the same wherever it is asked for.
-template <int D, int R>
-int workers(const SpanArgs &a) {
-    const int64_t most = D == 64 ? 1024 : 512;
-    const int64_t rows = a.T * a.group, tiles = rows / R + (a.B < a.T ? a.B : a.T);
-    const int64_t blocks = (a.Tk + kKeys - 1) / kKeys + kTileCost / kKeys;
-    const double pieces = (double)tiles * a.G * (double)blocks / kLeast + 1;
-    return pieces < (double)most ? (int)pieces : (int)most;
-}
-
-template <int D, int R>
-size_t bytes(const SpanArgs &a) {
-    const int n = workers<D, R>(a);
-    return header_bytes(n) + (size_t)n * 2 * R * (D + 2) * 4;
-}
+// 64), or fewer where even the most keys that the shape allows make fewer pieces.
+template <int D>
+int workers(const SpanArgs &a) { return span_workers<kRows>(a, D == 64 ? 1024 : 512); }
 
 template <int D, bool PAGED>
 hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
-    const int n = workers<D, kRows>(a);
-    Shared *shared = static_cast<Shared *>(ws);
-    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + header_bytes(n));
-    float *stat = part + (size_t)n * 2 * kRows * D;
-    span_attention_kernel<D, PAGED><<<n, 256, 0, stream>>>(a, shared, part, stat);
+    const int n = workers<D>(a);
+    const Workspace<D, kRows> s(ws, n);
+    span_attention_kernel<D, PAGED><<<n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n == 1) return e;
-    constexpr int per = 256 / (D / 4);
-    join_kernel<D, kRows><<<dim3(n, kRows / per), 256, 0, stream>>>(a, shared, part, stat);
+    if (e != hipSuccess || n == 1 || !may_share(a)) return e;
+    join_rows_kernel<D><<<dim3(n, kRows / (4 * (256 / (D / 4)))), 256, 0, stream>>>(a, s.shared, s.part, s.stat);
     return hipGetLastError();
 }
 
 }  // namespace span
 
-size_t span_workspace(const SpanArgs &a) {
-    return a.D == 64 ? span::bytes<64, span::kRows>(a) : span::bytes<128, span::kRows>(a);
+size_t span_tile_workspace(const SpanArgs &a) {
+    return a.D == 64 ? Workspace<64, span::kRows>::bytes(span::workers<64>(a))
+                     : Workspace<128, span::kRows>::bytes(span::workers<128>(a));
 }
 
-hipError_t launch_span_attention(const SpanArgs &a, void *ws, hipStream_t stream) {
+hipError_t launch_span_tiles(const SpanArgs &a, void *ws, hipStream_t stream) {
     if (a.kv_len)
         return a.D == 64 ? span::launch<64, true>(a, ws, stream) : span::launch<128, true>(a, ws, stream);
     return a.D == 64 ? span::launch<64, false>(a, ws, stream) : span::launch<128, false>(a, ws, stream);

@@ -1,0 +1,426 @@
+// span_few.hip -- attention of few new tokens over a paged cache: at most 16 or 32
+// rows of a request and key head (row r: head r % group of token r / group), on
+// the bf16 matrix instruction (v_mfma_f32_16x16x32_bf16).
+//
+// Bound by reading the cache once.  A workgroup is one wave, four to a compute unit
+// (eight at D = 64), and goes over its piece of the line of all tiles
+// (span_plan.h) in units of 32 keys: K and V go from global memory straight into
+// the wave's own two LDS buffers, so a unit or two of each wave are in flight at any
+// time and no wave waits for another.  Scores are computed transposed, S^T = K
+// Q^T: a lane holds eight keys of one row, the maximum takes two lane exchanges,
+// and the weights come out as the operand of O^T = V^T P^T.
+#include "attention_tile.h"
+#include "span_plan.h"
+
+#include <type_traits>
+
+namespace svdq {
+
+namespace few {
+
+using namespace attn;
+
+constexpr int kUnit = 32;                          // keys
+
+template <int D>
+struct Lds {
+    static constexpr int TILE = kUnit * D * 2;     // bytes of K or V of a unit
+    uint8_t k[2][TILE];
+    uint8_t v[2][TILE];
+    Seq seqs[64];
+};
+
+// Both other 16-lane groups' and the other half's: the largest of the four lanes of a row.
+__device__ __forceinline__ float max_of_row(float x) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_both_halves(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+}
+__device__ __forceinline__ float sum_of_row(float x) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return sum_both_halves(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+}
+
+// LDS layout of V: the eight rows and two 16-byte segments that 32 lanes of the
+// transposing read touch lie in different banks.
+template <int D>
+__device__ __forceinline__ int swz_few(int row) {
+    return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3);
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(64, D == 64 ? 2 : 1)
+few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict__ part, float *__restrict__ stat) {
+    constexpr int R = 16 * NR, DK = D / 32, DT = D / 16;
+    constexpr int RPT = 512 / D, SEGS = D / 8;     // rows per 1 KB copy, 16-byte segments of a row
+    constexpr int COPIES = 16 / RPT;               // of 16 keys, K and V each
+    __shared__ __align__(1024) Lds<D> lds;
+    const int lane = threadIdx.x, g4 = lane >> 4, c16 = lane & 15;
+    const int w = blockIdx.x;
+    if (lane == 0) shared[w].parts = 0;
+    Piece<R> piece;
+    if (!piece.open(a, lds.seqs, w, (int)gridDim.x)) return;
+    Place<R> &at = piece.at;
+
+    const int cp_row = lane / SEGS, cp_slot = lane % SEGS;
+    uint32_t k_at[COPIES], v_at[COPIES];           // bytes from the first of 16 keys
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) {
+        const int row = c * RPT + cp_row;
+        k_at[c] = row * (D * 2) + 16 * (cp_slot ^ swz_k<D>(row));
+        v_at[c] = row * (D * 2) + 16 * (cp_slot ^ swz_few<D>(row));
+    }
+    const uint8_t *k_rd[DK], *v_rd[DT];
+#pragma unroll
+    for (int s = 0; s < DK; ++s) k_rd[s] = lds.k[0] + c16 * (D * 2) + 16 * ((4 * s + g4) ^ swz_k<D>(c16));
+    {
+        const int row = 4 * g4 + (c16 >> 2);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            v_rd[d] = lds.v[0] + row * (D * 2) + 16 * ((2 * d + ((c16 & 3) >> 1)) ^ swz_few<D>(row)) + 8 * (c16 & 1);
+    }
+    const uint32_t lds_k = lds_address(lds.k), lds_v = lds_address(lds.v);
+    const float scale_log2 = a.scale_log2;
+    const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k), *vb = reinterpret_cast<const uint8_t *>(a.v);
+
+    for (;;) {
+        const int64_t row0 = at.t * R, rows_left = (int64_t)at.s.nq * a.group - row0;
+        if (rows_left <= 0) return;                // (lengths that changed under the call)
+        const int rows = rows_left < R ? (int)rows_left : R;
+        const int tok0 = (int)quotient(row0, a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
+        const int nk = at.s.nk, see0 = a.causal ? nk - at.s.nq + 1 : nk;
+        auto limit_of = [&](int i) {               // keys that row i of the tile sees
+            const int n = see0 + (a.causal ? tok0 + (rem0 + i) / a.group : 0);
+            return n < 0 ? 0 : n < nk ? n : nk;
+        };
+        const int low = uniform(limit_of(0)), high = uniform(limit_of(rows - 1));
+        int limit[NR];
+        int64_t from[NR];                          // element of q's row, of out's
+        uint32_t to_tok[NR], to_sub[NR];
+        u32x4 qf[NR][DK];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = 16 * r + c16 < rows ? 16 * r + c16 : rows - 1;   // past the last: never stored
+            limit[r] = limit_of(row);
+            to_tok[r] = tok0 + (rem0 + row) / a.group;
+            to_sub[r] = (rem0 + row) % a.group;
+            const uint16_t *p = a.q + (int64_t)(at.s.q0 + to_tok[r]) * a.q_stride +
+                                (int64_t)(at.g * a.group + to_sub[r]) * D + 8 * g4;
+            bool odd = false;
+#pragma unroll
+            for (int s = 0; s < DK; ++s) {
+                qf[r][s] = *reinterpret_cast<const u32x4 *>(p + 32 * s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    odd |= (qf[r][s][j] & 0x7F80u) == 0x7F80u || (qf[r][s][j] & 0x7F800000u) == 0x7F800000u;
+            }
+            // A row with a value that is not finite becomes a row of NaN: scores of minus
+            // infinity alone would look like keys that it does not see.
+            uint64_t odds = __ballot(odd);
+            odds |= odds >> 32;
+            if (odds && ((odds >> c16 | odds >> (c16 + 16)) & 1))
+#pragma unroll
+                for (int s = 0; s < DK; ++s)
+                    qf[r][s] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+        }
+
+        const int first = 2 * at.block_at(piece.x0), last0 = 2 * at.block_at(piece.x1);
+        const int seen = (high + kUnit - 1) / kUnit, last = last0 < seen ? last0 : seen;   // units
+        const int32_t *table = a.tables + (int64_t)at.b * a.width;
+        // Lane l: the page of 16 keys, window 64 i0 + l.
+        int pages = -1, pages_next = -1;
+        uint64_t bad16 = 0;
+        auto read_pages = [&](int i0) {
+            const int n = (64 * i0 + lane) * 16;
+            return n < nk ? table[n >> a.page_shift] : -1;
+        };
+        auto take_pages = [&](int i0, int p) {
+            const bool good = p >= 0 && p < a.pages;
+            pages = good ? p : -1;
+            bad16 = __ballot(!good && (64 * i0 + lane) * 16 < nk);
+        };
+        bool full[2];                              // the buffer's copies were all issued
+        uint32_t bad[2];
+        // Rows at or past the sequence's keys, and those without a page, are not read: K is left as
+        // it is (its scores are masked, whatever they are), V is zero (the weights are zero,
+        // and zero times what is not finite would be NaN).
+        auto issue = [&](int u, auto buffer) {
+            constexpr int BUF = decltype(buffer)::value;
+            if (u == first) {
+                take_pages(u >> 5, read_pages(u >> 5));
+                pages_next = read_pages((u >> 5) + 1);
+            } else if ((u & 31) == 0) {
+                take_pages(u >> 5, pages_next);
+                pages_next = read_pages((u >> 5) + 1);
+            }
+            bad[BUF] = (uint32_t)(bad16 >> (2 * (u & 31))) & 3u;
+            full[BUF] = true;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n0 = u * kUnit + 16 * h;
+                const int page = __builtin_amdgcn_readlane(pages, 2 * (u & 31) + h);
+                const int left = page < 0 ? 0 : nk - n0;
+                const int64_t r = ((((int64_t)page * a.G + at.g) << a.page_shift) +
+                                   (n0 & ((1 << a.page_shift) - 1))) * (D * 2);
+                const uint8_t *k0 = uniform_pointer(kb + r), *v0 = uniform_pointer(vb + r);
+                const uint32_t kd = lds_k + BUF * Lds<D>::TILE + h * 16 * D * 2;
+                const uint32_t vd = lds_v + BUF * Lds<D>::TILE + h * 16 * D * 2;
+                if (__builtin_expect(left >= 16, 1)) {
+                    copies_in_flight(k0, k_at, kd);
+                    copies_in_flight(v0, v_at, vd);
+                } else {
+                    full[BUF] = false;
+#pragma unroll
+                    for (int c = 0; c < COPIES; ++c) {
+                        if (c * RPT + cp_row < left) {
+                            copy_in_flight(k0, k_at[c], kd + c * 1024);
+                            copy_in_flight(v0, v_at[c], vd + c * 1024);
+                        } else {
+                            *reinterpret_cast<u32x4 *>(lds.v[BUF] + h * 16 * D * 2 + c * 1024 + lane * 16) = u32x4{};
+                        }
+                    }
+                }
+            }
+        };
+
+        f32x4 o[DT][NR];
+        float m[NR], l[NR];
+        bool masked = false;
+        // CAREFUL: once more, with values of v that are not finite taken out of the units that
+        // have a mask, and a NaN put where a row gives one of them a weight (zero times such a
+        // value would reach the rows that do not see its key).
+        auto pass = [&](auto mode) {
+            constexpr bool careful = decltype(mode)::value;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                m[r] = -__builtin_inff();
+                l[r] = 0.0f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d][r] = f32x4{};
+            }
+            auto unit = [&](int u, auto buffer) {
+                constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
+                const int n0 = u * kUnit;
+                // this unit's copies: all but the other buffer's, which follow them
+                if (u + 1 < last && full[1 - BUF])
+                    wait_loads<4 * COPIES>();
+                else
+                    wait_loads<0>();
+                asm volatile("" ::: "memory");
+                f32x4 s[2][NR];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) s[t][r] = f32x4{};
+#pragma unroll
+                for (int x = 0; x < DK; ++x)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(k_rd[x] + AT + t * 16 * D * 2);
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) s[t][r] = mfma_bf16_16x16x32(kf, qf[r][x], s[t][r]);
+                    }
+                const bool edge = n0 + kUnit > low || bad[BUF] != 0;
+                if (edge) {
+                    masked = true;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int n = n0 + 16 * t + 4 * g4 + e;
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+                                if (n >= limit[r] || (bad[BUF] >> t & 1)) s[t][r][e] = -__builtin_inff();
+                        }
+                }
+                u32x4 p[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    float top = s[0][r][0];
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e / 4][r][e % 4]);
+                    top = max_of_row(top);
+                    // The running maximum moves only when a score passes it by more than 8 in the
+                    // exponent of two.
+                    if (__any((top - m[r]) * scale_log2 > 8.0f)) {
+                        const float m1 = fmaxf(m[r], top);
+                        const float f = m[r] == m1 ? 1.0f : __builtin_amdgcn_exp2f((m[r] - m1) * scale_log2);
+                        m[r] = m1;
+                        l[r] *= f;
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) o[d][r] *= f;
+                    }
+                    // A weight's exponent is (s - m) c where |m c| is large (exact where a weight
+                    // counts), otherwise s c - fl(m c) in one operation.  A row without a key so
+                    // far has m = -inf and no offset.
+                    float off = m[r] * scale_log2;
+                    const bool far = fabsf(off) > 1024.0f;
+                    if (__any(far)) {
+                        const float by = far && m[r] > -__builtin_inff() ? m[r] : 0.0f;
+                        off = far ? 0.0f : off;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) s[e / 4][r][e % 4] -= by;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s[e / 4][r][e % 4] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 4][r][e % 4], scale_log2, -off));
+                    // weights rounded to bf16, the operand beside V; the same go into their sum
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        p[r][x] = pack_bf16x2(s[x / 2][r][2 * (x & 1)], s[x / 2][r][2 * (x & 1) + 1]);
+                        l[r] = add_pair(p[r][x], l[r]);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    u32x4 vf;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const u32x2 y = read_transposed(v_rd[d] + AT + 16 * x * (D * 2));
+                        vf[2 * x] = y.x;
+                        vf[2 * x + 1] = y.y;
+                    }
+                    u32x4 odd = {};
+                    if (careful && edge)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const bool lo = (vf[j] & 0x7F80u) == 0x7F80u, hi = (vf[j] & 0x7F800000u) == 0x7F800000u;
+                            odd[j] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
+                            vf[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                        }
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        o[d][r] = mfma_bf16_16x16x32(vf, p[r], o[d][r]);
+                        if (careful && edge) {
+                            const f32x4 c = mfma_bf16_16x16x32(odd, p[r], f32x4{});
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (c[e] > 0.0f) o[d][r][e] = __builtin_nanf("");
+                        }
+                    }
+                }
+                // the buffer has been read: the unit after the next may go there
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (u + 2 < last) issue(u + 2, buffer);
+            };
+            if (first < last) issue(first, std::integral_constant<int, 0>());
+            if (first + 1 < last) issue(first + 1, std::integral_constant<int, 1>());
+            for (int u = first; u < last; u += 2) {
+                unit(u, std::integral_constant<int, 0>());
+                if (u + 1 < last) unit(u + 1, std::integral_constant<int, 1>());
+            }
+        };
+        pass(std::false_type());
+        float z = 0.0f;                            // NaN where something is not finite
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z = __builtin_fmaf(o[d][r][e], 0.0f, z);
+        if (__builtin_expect(__any(masked && z != z), 0)) pass(std::true_type());
+
+        const bool whole = piece.whole(), begins = piece.begins();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = 16 * r + c16;
+            const float sum = sum_of_row(l[r]);
+            if (row >= rows) continue;
+            if (whole) {
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                uint16_t *dst = a.out + ((int64_t)(at.s.q0 + to_tok[r]) * a.H + at.g * a.group + to_sub[r]) * D + 4 * g4;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<u32x2 *>(dst + 16 * d) =
+                        u32x2{pack_bf16x2(o[d][r][0] * inv, o[d][r][1] * inv), pack_bf16x2(o[d][r][2] * inv, o[d][r][3] * inv)};
+            } else {
+                const int64_t x = (int64_t)(2 * w + (begins ? 1 : 0)) * R + row;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<f32x4 *>(part + x * D + 16 * d + 4 * g4) = o[d][r];
+                if (g4 == 0) {
+                    stat[2 * x] = m[r];
+                    stat[2 * x + 1] = sum;
+                }
+            }
+        }
+        if (!whole && begins) {
+            Shared sh;
+            sh.parts = piece.parts();
+            sh.q0 = at.s.q0;
+            sh.g = at.g;
+            sh.rows = rows;
+            sh.row0 = row0;
+            sh.pad = 0;
+            shared[w] = sh;                        // (all lanes write the same)
+        }
+        if (!piece.next(a)) return;
+    }
+}
+
+// Joins the parts of the shared tile that begins in worker blockIdx.x's piece, a row at a
+// time: a tile over a long cache has hundreds of parts and few rows, so D / 4 lanes take
+// every 256 / (D / 4)-th part each, and their sums are joined through LDS.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+join_parts_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+                  const float *__restrict__ stat) {
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+    __shared__ Joined sums[GROUPS][LANES];
+    const int64_t w = blockIdx.x;
+    const Shared sh = shared[w];
+    if (sh.parts == 0) return;
+    const int grp = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    for (int r = blockIdx.y; r < sh.rows; r += gridDim.y) {
+        Joined j = Joined::none();
+#pragma unroll 8
+        for (int i = grp; i < sh.parts; i += GROUPS) {
+            const int64_t x = (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R + r;
+            const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
+            j.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c), a.scale_log2);
+        }
+        sums[grp][c] = j;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i) {
+                const Joined &x = sums[i][c];
+                j.add(x.m, x.l, x.o, a.scale_log2);
+            }
+            store_joined<D>(a, sh, r, c, j);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NR>
+int workers(const SpanArgs &a) { return span_workers<16 * NR>(a, D == 64 ? 2048 : 1024); }
+
+template <int D, int NR>
+hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
+    constexpr int R = 16 * NR;
+    const int n = workers<D, NR>(a);
+    const Workspace<D, R> s(ws, n);
+    few_attention_kernel<D, NR><<<n, 64, 0, stream>>>(a, s.shared, s.part, s.stat);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || n == 1 || !may_share(a)) return e;
+    const int64_t rows = (int64_t)a.max_new * a.group;
+    join_parts_kernel<D, R><<<dim3(n, rows < R ? (int)rows : R), 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    return hipGetLastError();
+}
+
+}  // namespace few
+
+size_t span_few_workspace(const SpanArgs &a) {
+    const bool one = (int64_t)a.max_new * a.group <= 16;
+    if (a.D == 64)
+        return one ? Workspace<64, 16>::bytes(few::workers<64, 1>(a)) : Workspace<64, 32>::bytes(few::workers<64, 2>(a));
+    return one ? Workspace<128, 16>::bytes(few::workers<128, 1>(a)) : Workspace<128, 32>::bytes(few::workers<128, 2>(a));
+}
+
+hipError_t launch_span_few(const SpanArgs &a, void *ws, hipStream_t stream) {
+    const bool one = (int64_t)a.max_new * a.group <= 16;
+    if (a.D == 64) return one ? few::launch<64, 1>(a, ws, stream) : few::launch<64, 2>(a, ws, stream);
+    return one ? few::launch<128, 1>(a, ws, stream) : few::launch<128, 2>(a, ws, stream);
+}
+
+}  // namespace svdq
