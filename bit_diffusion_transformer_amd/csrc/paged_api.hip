@@ -93,6 +93,8 @@ int32_t read_shape(const svdq_packed_shape *e, bool own_keys, SpanArgs &a) {
     a.G = e->kv_heads;
     a.D = e->head_dim;
     a.group = a.H / a.G;
+    a.inv_group = 1.0 / a.group;
+    a.inv_group_f = (float)a.inv_group;
     a.causal = e->causal;
     return check_line(a);
 }
@@ -116,6 +118,8 @@ int32_t read_shape(const svdq_paged_shape *e, SpanArgs &a) {
     a.G = e->kv_heads;
     a.D = e->head_dim;
     a.group = a.H / a.G;
+    a.inv_group = 1.0 / a.group;
+    a.inv_group_f = (float)a.inv_group;
     a.width = e->width;
     a.max_new = e->max_new;
     a.causal = e->causal;

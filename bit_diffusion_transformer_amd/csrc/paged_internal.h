@@ -23,6 +23,8 @@ struct SpanArgs {
     int B, H, G, D, group;
     int page_shift, width, max_new, causal;
     float scale_log2;                    // scale log2(e)
+    float inv_group_f;                   // 1 / group
+    double inv_group;
 };
 
 // Tiles of 128 rows; paged with at most 32 rows of a request and key head: a wave each.

@@ -77,24 +77,20 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
 
     for (;; ) {
         // ---- one tile, or the part of it that this piece of the line has
-        const int first = at.block_at(piece.x0), last = at.block_at(piece.x1);
-        const int64_t row0 = at.t * kRows, rows_left = (int64_t)at.s.nq * a.group - row0;
+        const int first = piece.first, last = piece.last;
+        const int64_t row0 = (int64_t)at.t * kRows, rows_left = (int64_t)at.s.nq * a.group - row0;
         if (rows_left <= 0) return;                // (lengths that changed under the call)
         const int rows = rows_left < kRows ? (int)rows_left : kRows;
-        const int tok0 = (int)quotient(row0, a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
-        const int nk = at.s.nk, see0 = a.causal ? nk - at.s.nq + 1 : nk;
-        // keys that row i of the tile sees
-        auto limit_of = [&](int i) {
-            const int n = see0 + (a.causal ? tok0 + (rem0 + i) / a.group : 0);
-            return n < 0 ? 0 : n < nk ? n : nk;
-        };
+        const int tok0 = token_of(a, (double)row0), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
+        const int nk = at.s.nk;
         const int mine = 32 * wave + col;
         const bool active = 32 * wave < rows;      // uniform over the wave
         const int row = mine < rows ? mine : rows - 1;   // rows past the last: never stored
-        const int limit = limit_of(row);
-        const int low = __builtin_amdgcn_readfirstlane(limit_of(active ? 32 * wave : rows - 1));
-        const int high = __builtin_amdgcn_readfirstlane(limit_of(32 * wave + 31 < rows ? 32 * wave + 31 : rows - 1));
-        const int tok = tok0 + (rem0 + row) / a.group, sub = (rem0 + row) % a.group;
+        const int ahead = token_of(a, rem0 + row), tok = tok0 + ahead, sub = rem0 + row - ahead * a.group;
+        // keys that the row sees: no more than the rows behind it
+        int limit = a.causal ? nk - at.s.nq + 1 + tok : nk;
+        limit = limit < 0 ? 0 : limit < nk ? limit : nk;
+        const int low = __builtin_amdgcn_readlane(limit, 0), high = __builtin_amdgcn_readlane(limit, 31);
 
         const uint8_t *kb, *vb;
         int pages = -1;                            // lane l: page of block i0 + l / 4, rows 16 (l % 4) on
@@ -108,7 +104,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
             vb = reinterpret_cast<const uint8_t *>(a.v + at.s.k0 * a.v_stride + (int64_t)at.g * D);
         }
         const int32_t *table = PAGED ? a.tables + (int64_t)at.b * a.width : nullptr;
-        auto read_pages = [&](int i0) {            // of 16 blocks
+        auto read_pages = [&](int i0) __attribute__((always_inline)) {            // of 16 blocks
             const int n = i0 * kKeys + 16 * lane;
             int p = -1;
             if (n < nk) p = table[n >> a.page_shift];
@@ -119,7 +115,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         // Rows at or past the sequence's keys, and those without a page, are not read: K is left
         // as it is (its scores are masked, whatever they are), V is zero (the weights are
         // zero, and zero times what is not finite would be NaN).
-        auto issue = [&](int i, auto buffer) {
+        auto issue = [&](int i, auto buffer) __attribute__((always_inline)) {
             constexpr int BUF = decltype(buffer)::value;
             const int n0 = i * kKeys + 16 * wave;
             int left = nk - n0;
@@ -138,8 +134,6 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 v0 = vb + n0 * v_row;
             }
             const uint32_t kd = lds_k + BUF * Lds<D>::TILE, vd = lds_v + BUF * Lds<D>::TILE;
-            k0 = uniform_pointer(k0);
-            v0 = uniform_pointer(v0);
             if (__builtin_expect(left >= 16, 1)) {
                 copies_in_flight(k0, k_at, kd);
                 copies_in_flight(v0, v_at, vd);
@@ -162,15 +156,15 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                                 (int64_t)(at.g * a.group + sub) * D + 8 * h2;
 #pragma unroll
             for (int s = 0; s < DK; ++s) qf[s] = *reinterpret_cast<const u32x4 *>(p + 16 * s);
+            if (first < last) issue(first, std::integral_constant<int, 0>());
             // A row with a value that is not finite becomes a row of NaN: scores of minus
             // infinity alone would look like keys that it does not see.
-            bool odd = false;
+            uint32_t odd = 0;
 #pragma unroll
             for (int s = 0; s < DK; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    odd |= (qf[s][j] & 0x7F80u) == 0x7F80u || (qf[s][j] & 0x7F800000u) == 0x7F800000u;
-            const uint64_t rows_odd = __ballot(odd);
+                for (int j = 0; j < 4; ++j) odd |= not_finite(qf[s][j]);
+            const uint64_t rows_odd = __ballot(odd != 0);
             if (rows_odd && ((rows_odd >> col | rows_odd >> (col + 32)) & 1))
 #pragma unroll
                 for (int s = 0; s < DK; ++s) qf[s] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
@@ -183,13 +177,13 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         // gone over once more with such values taken out of the blocks that have a mask, and a
         // NaN put where a row gives one of them a weight.
         bool masked = false;
-        auto pass = [&](auto mode) {
+        auto pass = [&](auto mode) __attribute__((always_inline)) {
             constexpr bool careful = decltype(mode)::value;
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[d] = f32x16{};
             m = -__builtin_inff();
             l = 0.0f;
-            auto block = [&](int i, auto buffer) {
+            auto block = [&](int i, auto buffer) __attribute__((always_inline)) {
                 constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
                 const int n0 = i * kKeys;
                 wait_loads<0>();
@@ -201,7 +195,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 {
                     // fragments two steps ahead of the products that use them
                     u32x4 kf[3][2];
-                    auto load = [&](int t) {
+                    auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)
                             kf[t % 3][kk] = *reinterpret_cast<const u32x4 *>(k_rd[t] + AT + 32 * kk * (D * 2));
@@ -220,7 +214,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 // V fragments of a step of 16 keys (kk, t): keys 0 .. 3 and 8 .. 11 past
                 // 4 h2, every 32-wide block of columns
                 u32x4 vf[2][DB];
-                auto load_v = [&](int st) {
+                auto load_v = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -312,10 +306,9 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                             }
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const bool lo = (x[j] & 0x7F80u) == 0x7F80u;
-                                const bool hi = (x[j] & 0x7F800000u) == 0x7F800000u;
-                                odd[j] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
-                                x[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                                const uint32_t f = not_finite(x[j]);     // 0x8000 of each half
+                                odd[j] = (f >> 15) * 0x3F80u;
+                                x[j] &= ~((f >> 15) * 0xFFFFu);
                             }
                             o[d] = mfma_bf16_32x32x16(x, ps, o[d]);
                             const f32x16 c = mfma_bf16_32x32x16(odd, ps, f32x16{});
@@ -333,7 +326,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                     for (int d = 0; d < DB; ++d) o[d] = mfma_bf16_32x32x16(vf[st & 1][d], p[st >> 1][st & 1], o[d]);
                 }
             };
-            if (first < last) issue(first, std::integral_constant<int, 0>());
+            if (careful && first < last) issue(first, std::integral_constant<int, 0>());
             for (int i = first; i < last; i += 2) {
                 block(i, std::integral_constant<int, 0>());
                 if (i + 1 < last) block(i + 1, std::integral_constant<int, 1>());
@@ -352,9 +345,9 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         }
 
         l = sum_both_halves(l);
-        if (!piece.whole()) {
+        if (!piece.whole) {
             // unnormalized sums fp32 [slot][row][D], maximum and sum [slot][row][2]
-            const bool begins = piece.begins();
+            const bool begins = piece.begins;
             if (mine < rows) {
                 const int64_t r = (int64_t)(2 * w + (begins ? 1 : 0)) * kRows + mine;
 #pragma unroll

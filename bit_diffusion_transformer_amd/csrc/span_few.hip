@@ -83,57 +83,40 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
     const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k), *vb = reinterpret_cast<const uint8_t *>(a.v);
 
     for (;;) {
-        const int64_t row0 = at.t * R, rows_left = (int64_t)at.s.nq * a.group - row0;
+        const int64_t row0 = (int64_t)at.t * R, rows_left = (int64_t)at.s.nq * a.group - row0;
         if (rows_left <= 0) return;                // (lengths that changed under the call)
         const int rows = rows_left < R ? (int)rows_left : R;
-        const int tok0 = (int)quotient(row0, a.group), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
-        const int nk = at.s.nk, see0 = a.causal ? nk - at.s.nq + 1 : nk;
-        auto limit_of = [&](int i) {               // keys that row i of the tile sees
-            const int n = see0 + (a.causal ? tok0 + (rem0 + i) / a.group : 0);
-            return n < 0 ? 0 : n < nk ? n : nk;
-        };
-        const int low = uniform(limit_of(0)), high = uniform(limit_of(rows - 1));
-        int limit[NR];
-        int64_t from[NR];                          // element of q's row, of out's
-        uint32_t to_tok[NR], to_sub[NR];
+        const int tok0 = token_of(a, (double)row0), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
+        const int nk = at.s.nk;
+        int limit[NR], to_tok[NR], to_sub[NR];
         u32x4 qf[NR][DK];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = 16 * r + c16 < rows ? 16 * r + c16 : rows - 1;   // past the last: never stored
-            limit[r] = limit_of(row);
-            to_tok[r] = tok0 + (rem0 + row) / a.group;
-            to_sub[r] = (rem0 + row) % a.group;
+            const int ahead = token_of(a, rem0 + row);
+            to_tok[r] = tok0 + ahead;
+            to_sub[r] = rem0 + row - ahead * a.group;
+            // keys that the row sees: no more than the rows behind it
+            const int n = a.causal ? nk - at.s.nq + 1 + to_tok[r] : nk;
+            limit[r] = n < 0 ? 0 : n < nk ? n : nk;
             const uint16_t *p = a.q + (int64_t)(at.s.q0 + to_tok[r]) * a.q_stride +
                                 (int64_t)(at.g * a.group + to_sub[r]) * D + 8 * g4;
-            bool odd = false;
 #pragma unroll
-            for (int s = 0; s < DK; ++s) {
-                qf[r][s] = *reinterpret_cast<const u32x4 *>(p + 32 * s);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    odd |= (qf[r][s][j] & 0x7F80u) == 0x7F80u || (qf[r][s][j] & 0x7F800000u) == 0x7F800000u;
-            }
-            // A row with a value that is not finite becomes a row of NaN: scores of minus
-            // infinity alone would look like keys that it does not see.
-            uint64_t odds = __ballot(odd);
-            odds |= odds >> 32;
-            if (odds && ((odds >> c16 | odds >> (c16 + 16)) & 1))
-#pragma unroll
-                for (int s = 0; s < DK; ++s)
-                    qf[r][s] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+            for (int s = 0; s < DK; ++s) qf[r][s] = *reinterpret_cast<const u32x4 *>(p + 32 * s);
         }
+        const int low = __builtin_amdgcn_readlane(limit[0], 0), high = __builtin_amdgcn_readlane(limit[NR - 1], 15);
 
-        const int first = 2 * at.block_at(piece.x0), last0 = 2 * at.block_at(piece.x1);
-        const int seen = (high + kUnit - 1) / kUnit, last = last0 < seen ? last0 : seen;   // units
+        const int first = 2 * piece.first, seen = (high + kUnit - 1) / kUnit;
+        const int last = 2 * piece.last < seen ? 2 * piece.last : seen;   // units
         const int32_t *table = a.tables + (int64_t)at.b * a.width;
         // Lane l: the page of 16 keys, window 64 i0 + l.
         int pages = -1, pages_next = -1;
         uint64_t bad16 = 0;
-        auto read_pages = [&](int i0) {
+        auto read_pages = [&](int i0) __attribute__((always_inline)) {
             const int n = (64 * i0 + lane) * 16;
             return n < nk ? table[n >> a.page_shift] : -1;
         };
-        auto take_pages = [&](int i0, int p) {
+        auto take_pages = [&](int i0, int p) __attribute__((always_inline)) {
             const bool good = p >= 0 && p < a.pages;
             pages = good ? p : -1;
             bad16 = __ballot(!good && (64 * i0 + lane) * 16 < nk);
@@ -143,7 +126,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
         // Rows at or past the sequence's keys, and those without a page, are not read: K is left as
         // it is (its scores are masked, whatever they are), V is zero (the weights are zero,
         // and zero times what is not finite would be NaN).
-        auto issue = [&](int u, auto buffer) {
+        auto issue = [&](int u, auto buffer) __attribute__((always_inline)) {
             constexpr int BUF = decltype(buffer)::value;
             if (u == first) {
                 take_pages(u >> 5, read_pages(u >> 5));
@@ -161,7 +144,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                 const int left = page < 0 ? 0 : nk - n0;
                 const int64_t r = ((((int64_t)page * a.G + at.g) << a.page_shift) +
                                    (n0 & ((1 << a.page_shift) - 1))) * (D * 2);
-                const uint8_t *k0 = uniform_pointer(kb + r), *v0 = uniform_pointer(vb + r);
+                const uint8_t *k0 = kb + r, *v0 = vb + r;
                 const uint32_t kd = lds_k + BUF * Lds<D>::TILE + h * 16 * D * 2;
                 const uint32_t vd = lds_v + BUF * Lds<D>::TILE + h * 16 * D * 2;
                 if (__builtin_expect(left >= 16, 1)) {
@@ -182,13 +165,35 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
             }
         };
 
+        auto start = [&]() __attribute__((always_inline)) {
+            if (first < last) issue(first, std::integral_constant<int, 0>());
+            if (first + 1 < last) issue(first + 1, std::integral_constant<int, 1>());
+        };
+        start();
+        // A row with a value that is not finite becomes a row of NaN: scores of minus infinity
+        // alone would look like keys that it does not see.
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int s = 0; s < DK; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) odd |= not_finite(qf[r][s][j]);
+            uint64_t odds = __ballot(odd != 0);
+            odds |= odds >> 32;
+            if (odds && ((odds >> c16 | odds >> (c16 + 16)) & 1))
+#pragma unroll
+                for (int s = 0; s < DK; ++s)
+                    qf[r][s] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+        }
+
         f32x4 o[DT][NR];
         float m[NR], l[NR];
         bool masked = false;
         // CAREFUL: once more, with values of v that are not finite taken out of the units that
         // have a mask, and a NaN put where a row gives one of them a weight (zero times such a
         // value would reach the rows that do not see its key).
-        auto pass = [&](auto mode) {
+        auto pass = [&](auto mode) __attribute__((always_inline)) {
             constexpr bool careful = decltype(mode)::value;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -197,7 +202,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d][r] = f32x4{};
             }
-            auto unit = [&](int u, auto buffer) {
+            auto unit = [&](int u, auto buffer) __attribute__((always_inline)) {
                 constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
                 const int n0 = u * kUnit;
                 // this unit's copies: all but the other buffer's, which follow them
@@ -283,9 +288,9 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                     if (careful && edge)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const bool lo = (vf[j] & 0x7F80u) == 0x7F80u, hi = (vf[j] & 0x7F800000u) == 0x7F800000u;
-                            odd[j] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
-                            vf[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                            const uint32_t f = not_finite(vf[j]);        // 0x8000 of each half
+                            odd[j] = (f >> 15) * 0x3F80u;
+                            vf[j] &= ~((f >> 15) * 0xFFFFu);
                         }
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
@@ -302,8 +307,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (u + 2 < last) issue(u + 2, buffer);
             };
-            if (first < last) issue(first, std::integral_constant<int, 0>());
-            if (first + 1 < last) issue(first + 1, std::integral_constant<int, 1>());
+            if (careful) start();
             for (int u = first; u < last; u += 2) {
                 unit(u, std::integral_constant<int, 0>());
                 if (u + 1 < last) unit(u + 1, std::integral_constant<int, 1>());
@@ -319,7 +323,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                 for (int e = 0; e < 4; ++e) z = __builtin_fmaf(o[d][r][e], 0.0f, z);
         if (__builtin_expect(__any(masked && z != z), 0)) pass(std::true_type());
 
-        const bool whole = piece.whole(), begins = piece.begins();
+        const bool whole = piece.whole, begins = piece.begins;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = 16 * r + c16;

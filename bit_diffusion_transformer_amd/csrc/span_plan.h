@@ -11,9 +11,11 @@
 // tiles see all keys give every worker the same time, without the host knowing
 // a length.
 //
-// Lengths along the line are in keys times group, closed form: tile t of a
-// sequence is A + S t long (S = R with `causal`: R rows are R / group tokens, so
-// many more keys; S = 0 without).  Every worker computes the same cuts.
+// Positions are in keys times group, whole numbers below 2^52 in 64-bit floating
+// point (exact; a 64-bit integer product or quotient takes many times as long, and
+// a short call is mostly this): tile t of a sequence is c0 + S t long (S = R with
+// `causal`: R rows are R / group tokens, so many more keys; S = 0 without).  Cuts
+// are anywhere, but every worker computes them in the same way.
 #pragma once
 
 #include "paged_internal.h"
@@ -49,150 +51,131 @@ __device__ __forceinline__ Seq load_seq(const SpanArgs &a, int b) {
 
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)x) | (uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32);
+__device__ __forceinline__ double uniform(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)uniform((int)u) |
+                                          (uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32);
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, lane) |
+                                          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane) << 32);
 }
 
-// floor(x / y), 0 <= x < 2^52, 0 < y < 2^52: a 64-bit division takes several times as
-// long.  (Both are exact in 64-bit floating point; the quotient may round up to the next
-// whole number.)
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    const int64_t q = (int64_t)((double)x / (double)y);
-    return uniform(q * y > x ? q - 1 : q);
+// Inclusive sums over the lanes: within rows of 16, then rows 1 and 3 get their
+// neighbour's, then the upper half the lower's.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+    return x + __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+__device__ __forceinline__ double scan(double x) {
+    x = scan_step<0x111, 0xF>(x);                  // one lane up
+    x = scan_step<0x112, 0xF>(x);                  // two
+    x = scan_step<0x114, 0xF>(x);
+    x = scan_step<0x118, 0xF>(x);
+    x = scan_step<0x142, 0xA>(x);                  // lane 15 of the row below
+    return scan_step<0x143, 0xC>(x);               // lane 31
 }
 
-template <int R>
-struct Line {
-    // of one sequence
-    __device__ static __forceinline__ int64_t tiles(const SpanArgs &a, const Seq &s) {
-        return ((int64_t)s.nq * a.group + R - 1) / R;
-    }
-    __device__ static __forceinline__ int64_t cost0(const SpanArgs &a, const Seq &s) {
-        const int keys = a.causal ? (s.nk > s.nq ? s.nk - s.nq : 0) : s.nk;
-        return ((int64_t)keys + kTileCost) * a.group + (a.causal ? R : 0);
-    }
-    __device__ static __forceinline__ int64_t cost(const SpanArgs &a, int64_t c0, int64_t t) {
-        return a.causal ? c0 + R * t : c0;
-    }
-    __device__ static __forceinline__ int64_t before(const SpanArgs &a, int64_t c0, int64_t t) {
-        return c0 * t + (a.causal ? R * (t * (t - 1) / 2) : 0);
-    }
-    __device__ static __forceinline__ int64_t length(const SpanArgs &a, const Seq &s) {
-        return before(a, cost0(a, s), tiles(a, s));
-    }
-    // The tile that holds position x of the sequence's part of the line: the root of
-    // before(t) = x, to the whole number below, and mended.
-    __device__ static __forceinline__ int64_t tile_at(const SpanArgs &a, int64_t c0, int64_t count, int64_t x) {
-        int64_t t;
-        if (a.causal) {
-            const double h = (double)c0 - 0.5 * R;
-            t = uniform((int64_t)((sqrt(h * h + 2.0 * R * (double)x) - h) * (1.0 / R)));
-        } else {
-            t = quotient(x, c0);
-        }
-        t = t < 0 ? 0 : t < count ? t : count - 1;
-        while (t > 0 && before(a, c0, t) > x) --t;
-        while (t + 1 < count && before(a, c0, t + 1) <= x) ++t;
-        return t;
-    }
-    // Blocks of keys that tile t needs.
-    __device__ static __forceinline__ int blocks(const SpanArgs &a, const Seq &s, int64_t t) {
-        int keys = s.nk;
-        if (a.causal) {
-            const int64_t all = (int64_t)s.nq * a.group, row = (t + 1) * R < all ? (t + 1) * R : all;
-            const int64_t n = (int64_t)s.nk - s.nq + quotient(row - 1, a.group) + 1;
-            keys = n < 0 ? 0 : n < keys ? (int)n : keys;
-        }
-        return (keys + kKeys - 1) / kKeys;
-    }
-};
+// The token of row x of a sequence: floor(x / group), x < 2^34.
+__device__ __forceinline__ int token_of(const SpanArgs &a, double x) {
+    const int q = (int)((x + 0.5) * a.inv_group);
+    return uniform(q);
+}
+// The same for x < 2^16.
+__device__ __forceinline__ int token_of(const SpanArgs &a, int x) {
+    return (int)(((float)x + 0.5f) * a.inv_group_f);
+}
 
 // A place on the line: a tile (all values uniform over the wave).  `seqs` (LDS) holds the
-// 64 sequences from `chunk` on; every wave writes and reads the same there.
+// 64 sequences from `chunk` on, for this wave alone.
 template <int R>
 struct Place {
     Seq *seqs;
     Seq s;
-    int64_t head;                  // length of the line of one key head
-    int64_t t, begin, end;         // tile of the sequence; its part of the line
-    int64_t c0, count;             // of the sequence: first tile's length, tiles
-    int b, g, nb, chunk;
+    double head;                   // length of the line of one key head
+    double begin, end;             // the tile's part of the line
+    double c0;                     // length of the sequence's first tile
+    int t, count;                  // tile of the sequence, its tiles
+    int b, g, nb, chunk;           // sequence, key head, blocks of keys; first sequence in LDS
 
-    // The 64 sequences from b0 on: to LDS; -> this lane's part of the line.
-    __device__ int64_t load_chunk(const SpanArgs &a, int b0) {
+    __device__ static __forceinline__ double step(const SpanArgs &a) { return a.causal ? R : 0.0; }
+    __device__ static __forceinline__ double tiles(const SpanArgs &a, const Seq &v) {
+        return floor(((double)v.nq * a.group + (R - 1)) * (1.0 / R));
+    }
+    __device__ static __forceinline__ double cost0(const SpanArgs &a, const Seq &v) {
+        const int less = a.causal ? v.nq : 0;
+        return ((double)(v.nk > less ? v.nk - less : 0) + kTileCost) * a.group + step(a);
+    }
+    __device__ static __forceinline__ double before(const SpanArgs &a, double c, double n) {
+        return c * n + step(a) * 0.5 * (n * (n - 1.0));
+    }
+
+    // The 64 sequences from b0 on: to LDS; -> the sums of their lengths up to this lane's.
+    __device__ __forceinline__ double load_chunk(const SpanArgs &a, int b0) {
         const int lane = threadIdx.x & 63;
         chunk = b0;
         Seq v = {0, 0, 0, 0};
         if (b0 + lane < a.B) v = load_seq(a, b0 + lane);
         seqs[lane] = v;
-        return Line<R>::length(a, v);
+        return scan(before(a, cost0(a, v), tiles(a, v)));
     }
-    __device__ static int64_t scan(int64_t x) {    // inclusive sums over the lanes
-        const int lane = threadIdx.x & 63;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(x, d);
-            if (lane >= d) x += o;
-        }
-        return x;
-    }
-
-    // The whole line's length, and where x0 and x1 of it are: this tile becomes x0's, both are
-    // moved by snap.  cut(total, x0, x1) gives them (false: nothing to do).
-    template <class Cut>
-    __device__ bool open(const SpanArgs &a, Seq *lds, int64_t &x0, int64_t &x1, Cut cut) {
-        seqs = lds;
-        int64_t sum = scan(load_chunk(a, 0));
-        head = uniform(__shfl(sum, 63));
-        for (int b0 = 64; b0 < a.B; b0 += 64) {
-            sum = scan(load_chunk(a, b0));
-            head += uniform(__shfl(sum, 63));
-        }
-        if (head <= 0 || !cut(head * a.G, x0, x1)) return false;
-        const bool last = x1 >= head * a.G;
-        // x1 first: this object ends as x0's
-        if (!last) {
-            find(a, sum, x1);
-            x1 = snap(x1);
-        }
-        find(a, sum, x0);
-        if (x0 > 0) x0 = snap(x0);
-        return x0 < x1 && (x0 < end || next(a));
-    }
-    // The tile that holds position x; sum: the first chunk's, where there is only one.
-    __device__ void find(const SpanArgs &a, int64_t sum, int64_t x) {
-        g = (int)quotient(x, head);
-        int64_t base = g * head;
-        b = a.B - 1;
-        for (int b0 = 0;; b0 += 64) {
-            if (a.B > 64) sum = scan(load_chunk(a, b0));
-            const uint64_t past = __ballot(base + sum > x);
-            if (past) {
-                const int l = __builtin_ctzll(past);
-                b = b0 + l;
-                if (l > 0) base += uniform(__shfl(sum, l - 1));
-                break;
-            }
-            if (b0 + 64 >= a.B) break;
-            base += uniform(__shfl(sum, 63));
-        }
-        load(a);
-        t = count > 0 ? Line<R>::tile_at(a, c0, count, x - base) : 0;
-        begin = base + Line<R>::before(a, c0, t);
-        end = begin + Line<R>::cost(a, c0, t);
-        nb = Line<R>::blocks(a, s, t);
-    }
-    __device__ void load(const SpanArgs &a) {
+    // The sequence b and the key head g, whose part of the line begins at `base`; the tile that
+    // holds x.
+    __device__ __forceinline__ void load(const SpanArgs &a) {
         const Seq v = seqs[b - chunk];
         s.q0 = uniform(v.q0);
         s.nq = uniform(v.nq);
         s.k0 = uniform(v.k0);
         s.nk = uniform(v.nk);
-        count = Line<R>::tiles(a, s);
-        c0 = Line<R>::cost0(a, s);
+        count = uniform((int)tiles(a, s));
+        c0 = uniform(cost0(a, s));
+    }
+    __device__ __forceinline__ void set_tile(const SpanArgs &a, double at) {
+        begin = at;
+        end = uniform(at + c0 + step(a) * t);
+        int keys = s.nk;
+        if (a.causal) {
+            const double all = (double)s.nq * a.group, row = (double)(t + 1) * R;
+            const int n = s.nk - s.nq + token_of(a, (row < all ? row : all) - 1.0) + 1;
+            keys = n < 0 ? 0 : n < keys ? n : keys;
+        }
+        nb = (keys + kKeys - 1) / kKeys;
+    }
+    // The tile that holds position x (0 <= x < G head); sum: load_chunk's of the first chunk,
+    // where there is only one.
+    __device__ __forceinline__ void find(const SpanArgs &a, double sum, double x) {
+        g = uniform((int)(x * __builtin_amdgcn_rcp(head)));
+        while (g > 0 && g * head > x) --g;
+        while (g + 1 < a.G && (g + 1) * head <= x) ++g;
+        double base = g * head;
+        b = a.B - 1;
+        for (int b0 = 0;; b0 += 64) {
+            if (a.B > 64) sum = load_chunk(a, b0);
+            const uint64_t past = __ballot(base + sum > x);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                b = b0 + l;
+                if (l > 0) base += lane_of(sum, l - 1);
+                break;
+            }
+            if (b0 + 64 >= a.B) break;
+            base += lane_of(sum, 63);
+        }
+        load(a);
+        // the root of before(t) = x - base, from 32 bits and mended
+        const float h = (float)(c0 - 0.5 * step(a)), y = (float)(x - base);
+        t = uniform((int)(2.0f * y / (h + sqrtf(h * h + 2.0f * (float)step(a) * y))));
+        t = t < 0 ? 0 : t < count ? t : count > 0 ? count - 1 : 0;
+        while (t > 0 && base + before(a, c0, t) > x) --t;
+        while (t + 1 < count && base + before(a, c0, t + 1) <= x) ++t;
+        set_tile(a, uniform(base + before(a, c0, t)));
     }
     // The next tile of the line; false behind the last.
-    __device__ bool next(const SpanArgs &a) {
+    __device__ __forceinline__ bool next(const SpanArgs &a) {
         ++t;
         while (t >= count) {
             if (++b >= a.B) {
@@ -203,67 +186,75 @@ struct Place {
             load(a);
             t = 0;
         }
-        begin = end;
-        end = begin + Line<R>::cost(a, c0, t);
-        nb = Line<R>::blocks(a, s, t);
+        set_tile(a, end);
         return true;
     }
     // The block in front of which position x cuts this tile.
-    __device__ int block_at(int64_t x) const {
-        if (x <= begin || x >= end) return x <= begin ? 0 : nb;
-        const int i = uniform((int)((double)(x - begin) * nb / (double)(end - begin)));
+    __device__ __forceinline__ int block_at(double x) const {
+        if (x <= begin) return 0;
+        if (x >= end) return nb;
+        const int i = uniform((int)((x - begin) * nb * __builtin_amdgcn_rcp(end - begin)));
         return i < nb ? i : nb;
     }
     // x, moved to an end of the tile that has fewer than kLeast blocks on one side of it.
-    __device__ int64_t snap(int64_t x) const {
+    __device__ __forceinline__ double snap(double x) const {
         const int i = block_at(x);
         return i < kLeast ? begin : nb - i < kLeast ? end : x;
     }
 };
 
-// The cuts: worker w has the line from cut(w) to cut(w + 1).
-struct Cuts {
-    int64_t each, more;            // the first `more` workers have one more
-    int workers;
-    __device__ Cuts(int64_t total, int64_t least, int most) {
-        const int64_t n = quotient(total, least);
-        workers = n < 1 ? 1 : n < most ? (int)n : most;
-        each = quotient(total, workers);
-        more = total - each * workers;
-    }
-    __device__ int64_t at(int64_t w) const { return w * each + (w < more ? w : more); }
-};
-
-// A worker's piece of the line: its first tile, and where the piece ends.
+// A worker's piece of the line, tile by tile: the tile `at`, of which the piece has the
+// blocks first .. last - 1.
 template <int R>
 struct Piece {
     Place<R> at;
-    int64_t x0, x1;
-    int64_t each, more;            // of the cuts
-    int w;
-    __device__ bool open(const SpanArgs &a, Seq *lds, int worker, int most) {
+    double x0, x1, total;
+    int w, workers;
+    int first, last;
+    bool begins, whole;            // the piece has the tile's begin; all of it
+
+    __device__ __forceinline__ double cut(int i) const { return i < workers ? total * i * __builtin_amdgcn_rcp((double)workers) : total; }
+
+    __device__ __forceinline__ bool open(const SpanArgs &a, Seq *lds, int worker, int most) {
         w = worker;
-        return at.open(a, lds, x0, x1, [&](int64_t total, int64_t &from, int64_t &to) {
-            const Cuts c(total, (int64_t)kLeast * kKeys * a.group, most);
-            each = c.each;
-            more = c.more;
-            if (w >= c.workers) return false;
-            from = c.at(w);
-            to = c.at(w + 1);
-            return true;
-        });
+        at.seqs = lds;
+        double sum = at.load_chunk(a, 0);
+        at.head = lane_of(sum, 63);
+        for (int b0 = 64; b0 < a.B; b0 += 64) {
+            sum = at.load_chunk(a, b0);
+            at.head += lane_of(sum, 63);
+        }
+        total = uniform(at.head * a.G);
+        if (!(total > 0.0)) return false;
+        const double n = total * a.inv_group * (1.0 / (kLeast * kKeys));
+        workers = uniform(n < 1.0 ? 1 : n < (double)most ? (int)n : most);
+        if (w >= workers) return false;
+        x0 = uniform(cut(w));
+        x1 = uniform(cut(w + 1));
+        at.find(a, sum, x0);
+        if (w > 0) x0 = at.snap(x0);
+        if (x0 >= at.end && !at.next(a)) return false;
+        return enter();
     }
-    __device__ bool begins() const { return x0 <= at.begin; }    // the tile begins in this piece
-    __device__ bool whole() const { return begins() && x1 >= at.end; }
+    // This tile's part of the piece; false where the piece ends before it.
+    __device__ __forceinline__ bool enter() {
+        if (x1 < at.end) x1 = at.snap(x1);
+        begins = x0 <= at.begin;
+        whole = begins && x1 >= at.end;
+        first = at.block_at(x0);
+        last = at.block_at(x1);
+        return x1 > at.begin;
+    }
+    __device__ __forceinline__ bool next(const SpanArgs &a) { return x1 > at.end && at.next(a) && enter(); }
     // The workers that share the tile that begins here and ends outside: to the last whose cut
     // stays inside it.
-    __device__ int parts() const {
-        const int64_t y = more * (each + 1), x = at.end - 1;
-        int64_t z = x < y ? quotient(x, each + 1) : more + quotient(x - y, each);
-        while (z > w + 1 && at.snap(z * each + (z < more ? z : more)) >= at.end) --z;
-        return (int)(z - w) + 1;
+    __device__ __forceinline__ int parts() const {
+        int z = uniform((int)(at.end * workers * __builtin_amdgcn_rcp(total)));
+        z = z < workers ? z : workers - 1;
+        while (z + 1 < workers && cut(z + 1) < at.end) ++z;
+        while (z > w + 1 && (cut(z) >= at.end || at.snap(cut(z)) >= at.end)) --z;
+        return z - w + 1;
     }
-    __device__ bool next(const SpanArgs &a) { return x1 > at.end && at.next(a); }
 };
 
 // A tile whose keys are shared: by the worker that has the tile's begin.
