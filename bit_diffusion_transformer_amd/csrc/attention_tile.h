@@ -51,6 +51,9 @@ __device__ __forceinline__ void copy_in_flight(const uint8_t *base, uint32_t off
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
                  :: "v"(off), "s"(uniform_pointer(base)), "s"(__builtin_amdgcn_readfirstlane(to)) : "memory");
 }
+__device__ __forceinline__ void copies_in_flight(const uint8_t *base, const uint32_t (&off)[1], uint32_t to) {
+    copy_in_flight(base, off[0], to);
+}
 __device__ __forceinline__ void copies_in_flight(const uint8_t *base, const uint32_t (&off)[2], uint32_t to) {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %2\n\t"
                  "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"

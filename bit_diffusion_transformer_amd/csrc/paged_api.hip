@@ -62,7 +62,7 @@ int32_t read_pages(int32_t page, int64_t pages, int64_t width, int &shift) {
 // The line of all tiles has to fit 52 bits (span_plan.h).
 int32_t check_line(const SpanArgs &a) {
     const double tiles = (double)a.T * a.group / 16 + a.B;
-    const double each = a.group * ((double)a.Tk + 128) + (double)a.T * a.group + 128;
+    const double each = a.group * ((double)a.Tk + 256) + (double)a.T * a.group + 256;
     if (tiles * each * a.G > 0x1p52)
         return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%lld rows of %d sequences over %lld keys are too many",
                     (long long)a.T, a.B, (long long)a.Tk);

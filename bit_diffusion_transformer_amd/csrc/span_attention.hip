@@ -19,30 +19,29 @@ namespace span {
 
 using namespace attn;
 
-constexpr int kRows = 128;
-
-template <int D>
+template <int D, int WAVES>
 struct Lds {
     static constexpr int TILE = kKeys * D * 2;     // bytes of a K or V block
     uint8_t k[2][TILE];
     uint8_t v[2][TILE];
-    Seq seqs[4][64];                               // a wave each: they are not in step
+    Seq seqs[WAVES][64];                                // a wave each: they are not in step
 };
 
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(256, D == 64 ? 4 : 2)
+template <int D, bool PAGED, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, D == 64 ? 4 : 2)
 span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict__ part,
                       float *__restrict__ stat) {
+    constexpr int kRows = 32 * WAVES;
     constexpr int DB = D / 32, DK = D / 16;        // 32-wide blocks and 16-wide steps of D
     constexpr int RPT = 512 / D;                   // rows per 1 KB copy
     constexpr int SEGS = D / 8;                    // 16-byte segments of a row
-    constexpr int COPIES = kKeys / RPT / 4;        // copies per wave, K and V each: 16 rows
-    __shared__ __align__(1024) Lds<D> lds;
+    constexpr int PART = kKeys / WAVES, COPIES = PART / RPT;   // rows and copies per wave
+    __shared__ __align__(1024) Lds<D, WAVES> lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5, col = lane & 31;
 
     const int w = (int)xcd_range(blockIdx.x, gridDim.x);
-    if (threadIdx.x == 0) shared[w].parts = 0;
+    if (threadIdx.x == 0) shared[2 * w].parts = shared[2 * w + 1].parts = 0;
     Piece<kRows> piece;
     if (!piece.open(a, lds.seqs[wave], w, (int)gridDim.x)) return;
     Place<kRows> &at = piece.at;
@@ -53,7 +52,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     uint32_t k_at[COPIES], v_at[COPIES];
 #pragma unroll
     for (int c = 0; c < COPIES; ++c) {
-        const int r = c * RPT + cp_row, row = 16 * wave + r;
+        const int r = c * RPT + cp_row, row = PART * wave + r;
         k_at[c] = (uint32_t)(r * k_row) + 16 * (cp_slot ^ swz_k<D>(row));
         v_at[c] = (uint32_t)(r * v_row) + 16 * (cp_slot ^ swz_v<D>(row));
     }
@@ -117,12 +116,12 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         // zero, and zero times what is not finite would be NaN).
         auto issue = [&](int i, auto buffer) __attribute__((always_inline)) {
             constexpr int BUF = decltype(buffer)::value;
-            const int n0 = i * kKeys + 16 * wave;
+            const int n0 = i * kKeys + PART * wave;
             int left = nk - n0;
             const uint8_t *k0, *v0;
             if (PAGED) {
                 if ((i & 15) == 0 || i == first) read_pages(i & ~15);
-                const int page = __builtin_amdgcn_readlane(pages, 4 * (i & 15) + wave);
+                const int page = __builtin_amdgcn_readlane(pages, 4 * (i & 15) + wave * PART / 16);
                 bad_next = (uint32_t)(bad16 >> (4 * (i & 15))) & 15u;
                 if (page < 0) left = 0;
                 const int64_t r = ((((int64_t)page * a.G + at.g) << a.page_shift) +
@@ -133,8 +132,8 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 k0 = kb + n0 * k_row;
                 v0 = vb + n0 * v_row;
             }
-            const uint32_t kd = lds_k + BUF * Lds<D>::TILE, vd = lds_v + BUF * Lds<D>::TILE;
-            if (__builtin_expect(left >= 16, 1)) {
+            const uint32_t kd = lds_k + BUF * Lds<D, WAVES>::TILE, vd = lds_v + BUF * Lds<D, WAVES>::TILE;
+            if (__builtin_expect(left >= PART, 1)) {
                 copies_in_flight(k0, k_at, kd);
                 copies_in_flight(v0, v_at, vd);
             } else {
@@ -184,7 +183,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
             m = -__builtin_inff();
             l = 0.0f;
             auto block = [&](int i, auto buffer) __attribute__((always_inline)) {
-                constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D>::TILE;
+                constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D, WAVES>::TILE;
                 const int n0 = i * kKeys;
                 wait_loads<0>();
                 wave_barrier_all();
@@ -345,11 +344,11 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         }
 
         l = sum_both_halves(l);
-        if (!piece.whole) {
+        const int slot = share(piece, row0, rows, shared);
+        if (slot >= 0) {
             // unnormalized sums fp32 [slot][row][D], maximum and sum [slot][row][2]
-            const bool begins = piece.begins;
             if (mine < rows) {
-                const int64_t r = (int64_t)(2 * w + (begins ? 1 : 0)) * kRows + mine;
+                const int64_t r = (int64_t)slot * kRows + mine;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -360,16 +359,6 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                     stat[2 * r] = m;
                     stat[2 * r + 1] = l;
                 }
-            }
-            if (begins && threadIdx.x < 64) {        // (all lanes write the same)
-                Shared sh;
-                sh.parts = piece.parts();
-                sh.q0 = at.s.q0;
-                sh.g = at.g;
-                sh.rows = rows;
-                sh.row0 = row0;
-                sh.pad = 0;
-                shared[w] = sh;
             }
         } else {
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -397,61 +386,47 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     }
 }
 
-// Joins the parts of the shared tile that begins in worker blockIdx.x's piece: the
-// largest maximum, weights 2^(m_i - m) on sums and results.  D / 4 lanes per row,
-// four rows of a thread at once: a tile of prompts has two or three parts, and
-// its 128 rows are what has to be in flight.
-template <int D>
-__global__ void __launch_bounds__(256)
-join_rows_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
-                 const float *__restrict__ stat) {
-    constexpr int LANES = D / 4, STEP = 256 / LANES;
-    const int64_t w = blockIdx.x;
-    const Shared sh = shared[w];
-    const int r0 = blockIdx.y * (4 * STEP) + threadIdx.x / LANES, c = threadIdx.x % LANES;
-    if (sh.parts == 0 || r0 >= sh.rows) return;
-    Joined j[4] = {Joined::none(), Joined::none(), Joined::none(), Joined::none()};
-#pragma unroll 2
-    for (int i = 0; i < sh.parts; ++i) {
-        const int64_t slot = (i == 0 ? 2 * w + 1 : 2 * (w + i)) * kRows;
-        f32x2 s[4];
-        f32x4 o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t r = slot + (r0 + u * STEP < sh.rows ? r0 + u * STEP : r0);
-            s[u] = *reinterpret_cast<const f32x2 *>(stat + 2 * r);
-            o[u] = *reinterpret_cast<const f32x4 *>(part + r * D + 4 * c);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) j[u].add(s[u].x, s[u].y, o[u], a.scale_log2);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        if (r0 + u * STEP < sh.rows) store_joined<D>(a, sh, r0 + u * STEP, c, j[u]);
+// Workers: as many workgroups as the compute units hold at once, two waves to a SIMD (four
+// at D = 64), or fewer where even the most keys that the shape allows make fewer pieces.
+template <int D, int WAVES>
+int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, (D == 64 ? 4096 : 2048) / WAVES); }
+
+// Tiles of 256 rows read K and V half as often as tiles of 128, and fill less well.  With many
+// pairs of a row and a key (half of them seen with `causal`), and over a cache, 256.  128 | 256 us,
+// D = 128: 32 heads on 8, causal, one prompt of 1000 39.8 | 43.5, 2000 67 | 68, 4000 174 | 171,
+// 8000 530 | 515; twelve of 1 to 2000 103 | 107; 24 heads, four images of 777 to 4096 342 | 317.
+// Paged, 12 heads, 2 x 1560 rows over 32760 734 | 677; 512 over 4608 64.3 | 64.9.
+bool wide(const SpanArgs &a) {
+    if (a.max_new > 0) return true;
+    const double pairs = (double)a.T * (double)a.Tk / a.B * a.H;
+    return pairs >= (a.causal ? 0x1p28 : 0x1p27);
 }
 
-// Workers: as many workgroups as the compute units hold at once (two each, four at D =
-// 64), or fewer where even the most keys that the shape allows make fewer pieces.
 template <int D>
-int workers(const SpanArgs &a) { return span_workers<kRows>(a, D == 64 ? 1024 : 512); }
+size_t bytes(const SpanArgs &a) {
+    return wide(a) ? Workspace<D, 256>::bytes(workers<D, 8>(a)) : Workspace<D, 128>::bytes(workers<D, 4>(a));
+}
+
+template <int D, bool PAGED, int WAVES>
+hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
+    constexpr int R = 32 * WAVES;
+    const int n = workers<D, WAVES>(a);
+    const Workspace<D, R> s(ws, n);
+    span_attention_kernel<D, PAGED, WAVES><<<n, 64 * WAVES, 0, stream>>>(a, s.shared, s.part, s.stat);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || n == 1 || !may_share<R>(a)) return e;
+    join_kernel<D, R><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    return hipGetLastError();
+}
 
 template <int D, bool PAGED>
 hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
-    const int n = workers<D>(a);
-    const Workspace<D, kRows> s(ws, n);
-    span_attention_kernel<D, PAGED><<<n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n == 1 || !may_share(a)) return e;
-    join_rows_kernel<D><<<dim3(n, kRows / (4 * (256 / (D / 4)))), 256, 0, stream>>>(a, s.shared, s.part, s.stat);
-    return hipGetLastError();
+    return wide(a) ? launch<D, PAGED, 8>(a, ws, stream) : launch<D, PAGED, 4>(a, ws, stream);
 }
 
 }  // namespace span
 
-size_t span_tile_workspace(const SpanArgs &a) {
-    return a.D == 64 ? Workspace<64, span::kRows>::bytes(span::workers<64>(a))
-                     : Workspace<128, span::kRows>::bytes(span::workers<128>(a));
-}
+size_t span_tile_workspace(const SpanArgs &a) { return a.D == 64 ? span::bytes<64>(a) : span::bytes<128>(a); }
 
 hipError_t launch_span_tiles(const SpanArgs &a, void *ws, hipStream_t stream) {
     if (a.kv_len)

@@ -56,7 +56,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
     __shared__ __align__(1024) Lds<D> lds;
     const int lane = threadIdx.x, g4 = lane >> 4, c16 = lane & 15;
     const int w = blockIdx.x;
-    if (lane == 0) shared[w].parts = 0;
+    if (lane == 0) shared[2 * w].parts = shared[2 * w + 1].parts = 0;
     Piece<R> piece;
     if (!piece.open(a, lds.seqs, w, (int)gridDim.x)) return;
     Place<R> &at = piece.at;
@@ -323,13 +323,13 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                 for (int e = 0; e < 4; ++e) z = __builtin_fmaf(o[d][r][e], 0.0f, z);
         if (__builtin_expect(__any(masked && z != z), 0)) pass(std::true_type());
 
-        const bool whole = piece.whole, begins = piece.begins;
+        const int slot = share(piece, row0, rows, shared);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = 16 * r + c16;
             const float sum = sum_of_row(l[r]);
             if (row >= rows) continue;
-            if (whole) {
+            if (slot < 0) {
                 const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
                 uint16_t *dst = a.out + ((int64_t)(at.s.q0 + to_tok[r]) * a.H + at.g * a.group + to_sub[r]) * D + 4 * g4;
 #pragma unroll
@@ -337,7 +337,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                     *reinterpret_cast<u32x2 *>(dst + 16 * d) =
                         u32x2{pack_bf16x2(o[d][r][0] * inv, o[d][r][1] * inv), pack_bf16x2(o[d][r][2] * inv, o[d][r][3] * inv)};
             } else {
-                const int64_t x = (int64_t)(2 * w + (begins ? 1 : 0)) * R + row;
+                const int64_t x = (int64_t)slot * R + row;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     *reinterpret_cast<f32x4 *>(part + x * D + 16 * d + 4 * g4) = o[d][r];
@@ -347,52 +347,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                 }
             }
         }
-        if (!whole && begins) {
-            Shared sh;
-            sh.parts = piece.parts();
-            sh.q0 = at.s.q0;
-            sh.g = at.g;
-            sh.rows = rows;
-            sh.row0 = row0;
-            sh.pad = 0;
-            shared[w] = sh;                        // (all lanes write the same)
-        }
         if (!piece.next(a)) return;
-    }
-}
-
-// Joins the parts of the shared tile that begins in worker blockIdx.x's piece, a row at a
-// time: a tile over a long cache has hundreds of parts and few rows, so D / 4 lanes take
-// every 256 / (D / 4)-th part each, and their sums are joined through LDS.
-template <int D, int R>
-__global__ void __launch_bounds__(256)
-join_parts_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
-                  const float *__restrict__ stat) {
-    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-    __shared__ Joined sums[GROUPS][LANES];
-    const int64_t w = blockIdx.x;
-    const Shared sh = shared[w];
-    if (sh.parts == 0) return;
-    const int grp = threadIdx.x / LANES, c = threadIdx.x % LANES;
-    for (int r = blockIdx.y; r < sh.rows; r += gridDim.y) {
-        Joined j = Joined::none();
-#pragma unroll 8
-        for (int i = grp; i < sh.parts; i += GROUPS) {
-            const int64_t x = (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R + r;
-            const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
-            j.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c), a.scale_log2);
-        }
-        sums[grp][c] = j;
-        __syncthreads();
-        if (grp == 0) {
-#pragma unroll
-            for (int i = 1; i < GROUPS; ++i) {
-                const Joined &x = sums[i][c];
-                j.add(x.m, x.l, x.o, a.scale_log2);
-            }
-            store_joined<D>(a, sh, r, c, j);
-        }
-        __syncthreads();
     }
 }
 
@@ -406,9 +361,8 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
     const Workspace<D, R> s(ws, n);
     few_attention_kernel<D, NR><<<n, 64, 0, stream>>>(a, s.shared, s.part, s.stat);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n == 1 || !may_share(a)) return e;
-    const int64_t rows = (int64_t)a.max_new * a.group;
-    join_parts_kernel<D, R><<<dim3(n, rows < R ? (int)rows : R), 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    if (e != hipSuccess || n == 1 || !may_share<R>(a)) return e;
+    join_kernel<D, R><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
     return hipGetLastError();
 }
 

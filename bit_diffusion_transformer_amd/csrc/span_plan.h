@@ -24,8 +24,15 @@
 namespace svdq {
 
 constexpr int kKeys = 64;          // keys of a block
-constexpr int kTileCost = 128;     // keys' time that a tile takes beside its keys
-constexpr int kLeast = 2;          // blocks on each side of a cut, at least
+// Of tiles of R rows.  kTileCost: keys' time that a tile takes beside its keys (its queries, its
+// first copies, its result).  kLeast: blocks on each side of a cut, at least.  Tiles of 128, cost
+// and least 128 and 2 | 256 and 4 | 384 and 4 | 128 and 8, us: 77 tokens, 12 heads of 64 9.4 | 9.3
+// | 9.4 | 19.4; 500 tokens, 24 heads 26.0 | 18.3 | 18.5 | 21.9; twelve prompts of 1 to 2000, 32
+// heads 105 | 103 | 112 | 104; 40 tokens over 4000 44 | 32 | 33 | 33.
+template <int R>
+constexpr int kTileCost = R < 128 ? 128 : 256;
+template <int R>
+constexpr int kLeast = R < 128 ? 2 : 4;
 
 struct Seq {
     int q0, nq, k0, nk;            // first row and rows of q, of k
@@ -108,7 +115,7 @@ struct Place {
     }
     __device__ static __forceinline__ double cost0(const SpanArgs &a, const Seq &v) {
         const int less = a.causal ? v.nq : 0;
-        return ((double)(v.nk > less ? v.nk - less : 0) + kTileCost) * a.group + step(a);
+        return ((double)(v.nk > less ? v.nk - less : 0) + kTileCost<R>) * a.group + step(a);
     }
     __device__ static __forceinline__ double before(const SpanArgs &a, double c, double n) {
         return c * n + step(a) * 0.5 * (n * (n - 1.0));
@@ -199,7 +206,7 @@ struct Place {
     // x, moved to an end of the tile that has fewer than kLeast blocks on one side of it.
     __device__ __forceinline__ double snap(double x) const {
         const int i = block_at(x);
-        return i < kLeast ? begin : nb - i < kLeast ? end : x;
+        return i < kLeast<R> ? begin : nb - i < kLeast<R> ? end : x;
     }
 };
 
@@ -226,7 +233,7 @@ struct Piece {
         }
         total = uniform(at.head * a.G);
         if (!(total > 0.0)) return false;
-        const double n = total * a.inv_group * (1.0 / (kLeast * kKeys));
+        const double n = total * a.inv_group * (1.0 / (kLeast<R> * kKeys));
         workers = uniform(n < 1.0 ? 1 : n < (double)most ? (int)n : most);
         if (w >= workers) return false;
         x0 = uniform(cut(w));
@@ -246,42 +253,63 @@ struct Piece {
         return x1 > at.begin;
     }
     __device__ __forceinline__ bool next(const SpanArgs &a) { return x1 > at.end && at.next(a) && enter(); }
-    // The workers that share the tile that begins here and ends outside: to the last whose cut
-    // stays inside it.
-    __device__ __forceinline__ int parts() const {
-        int z = uniform((int)(at.end * workers * __builtin_amdgcn_rcp(total)));
-        z = z < workers ? z : workers - 1;
-        while (z + 1 < workers && cut(z + 1) < at.end) ++z;
-        while (z > w + 1 && (cut(z) >= at.end || at.snap(cut(z)) >= at.end)) --z;
-        return z - w + 1;
+    // The pieces that share this tile: the last that begins at or before the tile's begin, and
+    // the last that begins before its end.  (A cut in another tile snaps to no further than
+    // this tile's ends.)
+    __device__ __forceinline__ int near(double x) const {
+        const int z = uniform((int)(x * workers * __builtin_amdgcn_rcp(total)));
+        return z < workers ? z : workers - 1;
+    }
+    __device__ __forceinline__ int first_piece() const {
+        if (begins) return w;
+        int z = near(at.begin);
+        while (z + 1 < w && (cut(z + 1) <= at.begin || at.snap(cut(z + 1)) <= at.begin)) ++z;
+        while (z > 0 && cut(z) > at.begin && at.snap(cut(z)) > at.begin) --z;
+        return z;
+    }
+    __device__ __forceinline__ int last_piece() const {
+        int z = near(at.end);
+        while (z + 1 < workers && cut(z + 1) < at.end && at.snap(cut(z + 1)) < at.end) ++z;
+        while (z > w && (cut(z) >= at.end || at.snap(cut(z)) >= at.end)) --z;
+        return z;
     }
 };
 
-// A tile whose keys are shared: by the worker that has the tile's begin.
+// A tile whose keys several pieces share, as one of them sees it.
 struct Shared {
-    int32_t parts;                 // workers; 0: no such tile
-    int32_t q0, g, rows;           // first row of the sequence, key head, rows of the tile
+    int32_t parts, index;          // pieces (0: no such tile), and which this one is
+    int32_t rows, q0, g, pad;      // rows of the tile, first row of its sequence, key head
     int64_t row0;                  // first row of the tile in its sequence
-    int64_t pad;
 };
 
-// The workspace: shared tiles' headers (one a worker), then partial results of R
-// rows, unnormalized sums and (maximum, sum) of the weights: two slots a worker,
-// 2 w + 1 for the tile that begins in its piece and ends outside, 2 w for the one
-// that began before.
+// For the tile that the piece is at, with `rows` rows from row0 on: the slot of its partial
+// result (-1: the tile is this piece's alone), and the slot's header.
+template <int R>
+__device__ __forceinline__ int share(const Piece<R> &p, int64_t row0, int rows, Shared *__restrict__ shared) {
+    if (p.whole) return -1;
+    const int slot = 2 * p.w + (p.begins ? 1 : 0);
+    const int first = p.first_piece(), last = p.last_piece();
+    if (threadIdx.x == 0) shared[slot] = Shared{last - first + 1, p.w - first, rows, p.at.s.q0, p.at.g, 0, row0};
+    return slot;
+}
+
+// The workspace: headers, then partial results of R rows, unnormalized sums and
+// (maximum, sum) of the weights: two slots a piece, 2 w + 1 for the tile that
+// begins in it and ends outside, 2 w for the one that began before.
 template <int D, int R>
 struct Workspace {
     Shared *shared;
     float *part, *stat;
-    static size_t head(int workers) { return align256((size_t)workers * sizeof(Shared)); }
-    static size_t bytes(int workers) { return head(workers) + (size_t)workers * 2 * R * (D + 2) * 4; }
-    Workspace(void *ws, int workers)
-        : shared(static_cast<Shared *>(ws)), part(reinterpret_cast<float *>(static_cast<char *>(ws) + head(workers))),
-          stat(part + (size_t)workers * 2 * R * D) {}
+    static size_t head(int pieces) { return align256((size_t)pieces * 2 * sizeof(Shared)); }
+    static size_t bytes(int pieces) { return head(pieces) + (size_t)pieces * 2 * R * (D + 2) * 4; }
+    Workspace(void *ws, int pieces)
+        : shared(static_cast<Shared *>(ws)), part(reinterpret_cast<float *>(static_cast<char *>(ws) + head(pieces))),
+          stat(part + (size_t)pieces * 2 * R * D) {}
 };
 
 // Can any tile be shared, with the most keys that the shape allows?
-inline bool may_share(const SpanArgs &a) { return a.Tk > (2 * kLeast - 1) * kKeys; }
+template <int R>
+bool may_share(const SpanArgs &a) { return a.Tk > (2 * kLeast<R> - 1) * kKeys; }
 
 // `most` workers, or fewer where the most keys that the shape allows make fewer pieces.
 // (`most` follows from the whole card's 256 compute units, not the current device's: the
@@ -289,8 +317,8 @@ inline bool may_share(const SpanArgs &a) { return a.Tk > (2 * kLeast - 1) * kKey
 template <int R>
 int span_workers(const SpanArgs &a, int most) {
     const double tiles = (double)(a.T * a.group / R + (a.B < a.T ? a.B : a.T));
-    const double blocks = (double)((a.Tk + kKeys - 1) / kKeys + kTileCost / kKeys);
-    const double pieces = tiles * a.G * blocks / kLeast + 1;
+    const double blocks = (double)((a.Tk + kKeys - 1) / kKeys + kTileCost<R> / kKeys);
+    const double pieces = tiles * a.G * blocks / kLeast<R> + 1;
     return pieces < most ? (int)pieces : most;
 }
 
@@ -319,6 +347,66 @@ __device__ __forceinline__ void store_joined(const SpanArgs &a, const Shared &sh
     const int64_t row = sh.row0 + r, tok = row / a.group;
     *reinterpret_cast<u32x2 *>(a.out + ((sh.q0 + tok) * a.H + sh.g * a.group + (row - tok * a.group)) * D + 4 * c) =
         u32x2{pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv)};
+}
+
+// Joins the shared tiles: a workgroup per slot, the i-th of a tile's P parts taking the
+// i-th of P ranges of its rows, so that each reads about one part's worth.  D / 4 lanes
+// per row; where a range has fewer rows than there are such groups of lanes, several
+// groups take a row's parts in turn and are joined through LDS.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+join_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+            const float *__restrict__ stat) {
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+    __shared__ Joined sums[GROUPS][LANES];
+    const Shared sh = shared[blockIdx.x];
+    if (sh.parts == 0) return;
+    const int r0 = (int)((int64_t)sh.rows * sh.index / sh.parts), r1 = (int)((int64_t)sh.rows * (sh.index + 1) / sh.parts);
+    const int grp = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    const int64_t w = (blockIdx.x >> 1) - sh.index;         // the piece with part 0
+    auto slot = [&](int i) { return (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R; };
+    int ways = 1;
+    while (2 * ways * (r1 - r0) <= GROUPS && 2 * ways <= GROUPS) ways *= 2;
+    if (ways > 1) {
+        const int r = r0 + grp / ways;
+        Joined j = Joined::none();
+        if (r < r1) {
+#pragma unroll 8
+            for (int i = grp % ways; i < sh.parts; i += ways) {
+                const int64_t x = slot(i) + r;
+                const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
+                j.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c), a.scale_log2);
+            }
+        }
+        sums[grp][c] = j;
+        __syncthreads();
+        if (r >= r1 || grp % ways != 0) return;
+        for (int i = 1; i < ways; ++i) {
+            const Joined &x = sums[grp + i][c];
+            j.add(x.m, x.l, x.o, a.scale_log2);
+        }
+        store_joined<D>(a, sh, r, c, j);
+        return;
+    }
+    for (int r = r0 + grp; r < r1; r += 4 * GROUPS) {
+        Joined j[4] = {Joined::none(), Joined::none(), Joined::none(), Joined::none()};
+#pragma unroll 2
+        for (int i = 0; i < sh.parts; ++i) {
+            f32x2 s[4];
+            f32x4 o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t x = slot(i) + (r + u * GROUPS < r1 ? r + u * GROUPS : r);
+                s[u] = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
+                o[u] = *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) j[u].add(s[u].x, s[u].y, o[u], a.scale_log2);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (r + u * GROUPS < r1) store_joined<D>(a, sh, r + u * GROUPS, c, j[u]);
+    }
 }
 
 }  // namespace svdq
