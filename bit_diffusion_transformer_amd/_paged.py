@@ -191,11 +191,8 @@ def page_tables(cached, added, free_pages, tables, page: int, pages: int, tokens
     if not 0 <= tokens < 1 << 31 or not 0 <= pages < 1 << 31 or not 0 < page <= MAX_PAGE:
         raise ValueError("page = %d, pages = %d, tokens = %d" % (page, pages, tokens))
     dev = one_device(cached=cached, added=added, free_pages=free_pages, tables=tables)
-    # one allocation, parts 16-byte aligned
-    sizes = (B + 1, B, tokens, tokens, 2)
-    each = [-(-n // 4) * 4 for n in sizes]
-    q_starts, kv_len, slots, positions, counts = (
-        t[:n] for t, n in zip(cached.new_empty(sum(each)).split(each), sizes))
+    q_starts, kv_len, slots, positions, counts = cached.new_empty(2 * (B + tokens) + 3).split(
+        (B + 1, B, tokens, tokens, 2))
     shape = TableShape(tokens, pages, F, B, page, width)
     with on(dev):
         _entries.call("svdq_page_tables", at(cached), at(added), at(free_pages), ctypes.byref(shape),

@@ -71,11 +71,12 @@ def one_device(**tensors: Optional[torch.Tensor]) -> torch.device:
     for what, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()
+        if i < 0:
             raise ValueError("%s must be on a GPU, is on %s" % (what, t.device))
         if first is None:
-            first, index = t, t.get_device()
-        elif t.get_device() != index:
+            first, index = t, i
+        elif i != index:
             raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, first.device))
     return first.device
 
