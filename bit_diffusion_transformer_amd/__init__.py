@@ -313,6 +313,47 @@ def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamm
                       out.get("bias"))
 
 
+def cached_attention(X, qkv: dict, out: dict, heads: int, kv_heads: int, head_dim: int, gamma_q, gamma_k,
+                     eps: float, cos_t, sin_t, k_cache, v_cache, tables, q_starts, kv_len, slots,
+                     positions, max_new: Optional[int] = None, causal: bool = True,
+                     half: bool = False) -> torch.Tensor:
+    """Y = out(paged_attention(qkv(X))): a step of the attention half over a paged cache, on two W4A4
+    layers (dicts with lam, L1, qw, sw, L2, bias), through svdq_linear, svdq_qkv_norm_rope_cache,
+    svdq_paged_attention and svdq_linear.  X bf16 [T, K]: the new tokens of all requests; the qkv
+    layer has (heads + 2 kv_heads) head_dim channels; the caches get the new keys and values.
+    q_starts, kv_len, slots and positions from page_tables; the other arguments as for
+    qkv_norm_rope_cache and paged_attention.  Rows of no request are unspecified.  Every tensor is
+    checked first."""
+    T, K = expect(X, "X", BF16, (None, None))
+    HD = heads * head_dim
+    pages, _, page, _ = expect(k_cache, "k_cache", BF16, (None, kv_heads, None, head_dim))
+    expect(v_cache, "v_cache", BF16, (pages, kv_heads, page, head_dim))
+    B = expect(tables, "tables", I32, (None, None))[0]
+    expect(q_starts, "q_starts", I32, (B + 1,))
+    expect(kv_len, "kv_len", I32, (B,))
+    expect(slots, "slots", I32, (T,))
+    expect(positions, "positions", I32, (T,))
+    expect(sin_t, "sin_t", F32, tuple(expect(cos_t, "cos_t", F32, (None, None))))
+    tensors = {"X": X, "k_cache": k_cache, "v_cache": v_cache, "tables": tables, "q_starts": q_starts,
+               "kv_len": kv_len, "slots": slots, "positions": positions, "cos_t": cos_t, "sin_t": sin_t,
+               **_expect_layer(qkv, "qkv", K, (heads + 2 * kv_heads) * head_dim),
+               **_expect_layer(out, "out", HD, None)}
+    for what, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        if g is not None:
+            expect(g, what, BF16, (head_dim,))
+            tensors[what] = g
+    one = len({t.get_device() for t in tensors.values()}) == 1
+    dev = one_device(X=X) if one else one_device(**tensors)     # the latter raises
+    with on(dev):
+        P = linear(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"], qkv.get("bias"))
+        Q = qkv_norm_rope_cache(P, heads, kv_heads, gamma_q, gamma_k, eps, cos_t, sin_t, positions,
+                                slots, k_cache, v_cache, half=half)
+        A = paged_attention(Q, k_cache, v_cache, tables, q_starts, kv_len, max_new=max_new,
+                            causal=causal)
+        return linear(A.view(T, HD), out["lam"], out["L1"], out["qw"], out["sw"], out["L2"],
+                      out.get("bias"))
+
+
 def group_sums(qa, sa, qw, sw, M: int, N: int, m0: int, n0: int, tm: int,
                tn: int) -> torch.Tensor:
     """Exact per-group int32 sums of a block (test hook, through the GEMM's own tile code)

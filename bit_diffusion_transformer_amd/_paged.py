@@ -9,7 +9,7 @@ from typing import Optional
 import torch
 
 from ._tensors import (BF16, Entries, F32, F32T, I32, I32T, P, SZ, at, expect, expect_rows, on,
-                       one_device, ptr, scratch, stream_ptr)
+                       one_device, ptr, scratch, stream_of, stream_ptr)
 
 MIN_PAGE, MAX_PAGE = 16, 256
 MAX_SLOTS = 1 << 30
@@ -145,7 +145,7 @@ def packed_attention(q, k, v, q_starts, k_starts: Optional[torch.Tensor] = None,
     ws = scratch(workspace, need, dev)
     with on(dev):
         _entries.call("svdq_packed_attention", at(q), at(k), at(v), at(q_starts), at(k_starts),
-                      ctypes.byref(shape), _scale(scale, D), at(out), at(ws), need, stream_ptr())
+                      ctypes.byref(shape), _scale(scale, D), at(out), at(ws), need, stream_of(dev))
     return out
 
 
@@ -173,7 +173,7 @@ def paged_attention(q, k_cache, v_cache, tables, q_starts, kv_len, max_new: Opti
     with on(dev):
         _entries.call("svdq_paged_attention", at(q), at(k_cache), at(v_cache), at(tables),
                       at(q_starts), at(kv_len), ctypes.byref(shape), _scale(scale, D), at(out),
-                      at(ws), need, stream_ptr())
+                      at(ws), need, stream_of(dev))
     return out
 
 
@@ -191,13 +191,13 @@ def page_tables(cached, added, free_pages, tables, page: int, pages: int, tokens
     if not 0 <= tokens < 1 << 31 or not 0 <= pages < 1 << 31 or not 0 < page <= MAX_PAGE:
         raise ValueError("page = %d, pages = %d, tokens = %d" % (page, pages, tokens))
     dev = one_device(cached=cached, added=added, free_pages=free_pages, tables=tables)
-    q_starts, kv_len, slots, positions, counts = cached.new_empty(2 * (B + tokens) + 3).split(
-        (B + 1, B, tokens, tokens, 2))
+    q_starts, kv_len, slots, positions, counts = torch.split_with_sizes(
+        cached.new_empty(2 * (B + tokens) + 3), (B + 1, B, tokens, tokens, 2))
     shape = TableShape(tokens, pages, F, B, page, width)
     with on(dev):
         _entries.call("svdq_page_tables", at(cached), at(added), at(free_pages), ctypes.byref(shape),
                       at(tables), at(q_starts), at(kv_len), at(slots), at(positions), at(counts),
-                      stream_ptr())
+                      stream_of(dev))
     return q_starts, kv_len, slots, positions, counts
 
 
@@ -230,5 +230,5 @@ def qkv_norm_rope_cache(qkv, heads: int, kv_heads: int, gamma_q, gamma_k, eps: f
                         at(gamma_k), eps, at(cos_t), at(sin_t), at(positions), at(slots), at(out),
                         at(k_cache), at(v_cache))
     with on(dev):
-        _entries.call("svdq_qkv_norm_rope_cache", at(qkv), ctypes.byref(epi), stream_ptr())
+        _entries.call("svdq_qkv_norm_rope_cache", at(qkv), ctypes.byref(epi), stream_of(dev))
     return out

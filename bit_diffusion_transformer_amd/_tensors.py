@@ -115,6 +115,13 @@ def stream_ptr(stream=None):
     return _raw_stream(torch.cuda.current_device())
 
 
+def stream_of(dev: torch.device):
+    """The handle of the current stream of `dev`."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
+
+
 def scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
     """`workspace` if it holds `need` bytes on `dev`, otherwise a new one (None when need == 0)."""
     if need == 0:

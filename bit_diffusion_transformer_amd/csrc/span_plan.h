@@ -371,7 +371,7 @@ join_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restri
         const int r = r0 + grp / ways;
         Joined j = Joined::none();
         if (r < r1) {
-#pragma unroll 8
+#pragma unroll 16
             for (int i = grp % ways; i < sh.parts; i += ways) {
                 const int64_t x = slot(i) + r;
                 const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
