@@ -346,19 +346,19 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         l = sum_both_halves(l);
         const int slot = share(piece, row0, rows, shared);
         if (slot >= 0) {
-            // unnormalized sums fp32 [slot][row][D], maximum and sum [slot][row][2]
-            if (mine < rows) {
+            // Unnormalized sums, as the lanes hold them: [slot][wave][8 columns][lane][4] fp32, and
+            // maximum and sum of the weights [slot][row][2].
+            float *p = part + ((int64_t)slot * WAVES + wave) * (32 * D) + 4 * lane;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<f32x4 *>(p + (4 * d + e) * 256) =
+                        f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+            if (h2 == 0) {
                 const int64_t r = (int64_t)slot * kRows + mine;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<f32x4 *>(part + r * D + 32 * d + 8 * e + 4 * h2) =
-                            f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
-                if (h2 == 0) {
-                    stat[2 * r] = m;
-                    stat[2 * r + 1] = l;
-                }
+                stat[2 * r] = m;
+                stat[2 * r + 1] = l;
             }
         } else {
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -383,6 +383,38 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 }
         }
         if (!piece.next(a)) return;
+    }
+}
+
+// Joins the shared tiles: a workgroup per slot.  A tile is WAVES x D / 32 items of 32 rows
+// and 32 columns, of which the i-th of P parts takes the i-th of P ranges; 128 threads
+// an item, which read whole kilobytes of a part as its wave wrote them.
+template <int D, int WAVES>
+__global__ void __launch_bounds__(256)
+join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+                  const float *__restrict__ stat) {
+    constexpr int DB = D / 32, ITEMS = WAVES * DB;
+    const Shared sh = shared[blockIdx.x];
+    if (sh.parts == 0) return;
+    const int i0 = ITEMS * sh.index / sh.parts, i1 = ITEMS * (sh.index + 1) / sh.parts;
+    const int col = threadIdx.x & 31, e = (threadIdx.x >> 5) & 3;
+    const int64_t w = (blockIdx.x >> 1) - sh.index;         // the piece with part 0
+    for (int item = i0 + (threadIdx.x >> 7); item < i1; item += 2) {
+        const int wave = item / DB, db = item % DB, r = 32 * wave + col;
+        if (r >= sh.rows) continue;
+        Joined lo = Joined::none(), hi = Joined::none();    // 4 columns each
+#pragma unroll 4
+        for (int i = 0; i < sh.parts; ++i) {
+            const int64_t slot = i == 0 ? 2 * w + 1 : 2 * (w + i);
+            const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * (slot * (32 * WAVES) + r));
+            const float *p = part + (slot * WAVES + wave) * (32 * D) + (4 * db + e) * 256 + 4 * col;
+            lo.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(p), a.scale_log2);
+            hi.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(p + 128), a.scale_log2);
+        }
+        const float inv = lo.l > 0.0f ? 1.0f / lo.l : 0.0f;
+        *reinterpret_cast<u32x4 *>(joined_row<D>(a, sh, r) + 32 * db + 8 * e) =
+            u32x4{pack_bf16x2(lo.o.x * inv, lo.o.y * inv), pack_bf16x2(lo.o.z * inv, lo.o.w * inv),
+                  pack_bf16x2(hi.o.x * inv, hi.o.y * inv), pack_bf16x2(hi.o.z * inv, hi.o.w * inv)};
     }
 }
 
@@ -415,7 +447,7 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
     span_attention_kernel<D, PAGED, WAVES><<<n, 64 * WAVES, 0, stream>>>(a, s.shared, s.part, s.stat);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || n == 1 || !may_share<R>(a)) return e;
-    join_kernel<D, R><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    join_tiles_kernel<D, WAVES><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
     return hipGetLastError();
 }
 

@@ -2,8 +2,7 @@
 // rows of a request and key head (row r: head r % group of token r / group), on
 // the bf16 matrix instruction (v_mfma_f32_16x16x32_bf16).
 //
-// Bound by reading the cache once.  A workgroup is one wave, four to a compute unit
-// (eight at D = 64), and goes over its piece of the line of all tiles
+// Bound by reading the cache once.  A workgroup is one wave, and goes over its piece of the line of all tiles
 // (span_plan.h) in units of 32 keys: K and V go from global memory straight into
 // the wave's own two LDS buffers, so a unit or two of each wave are in flight at any
 // time and no wave waits for another.  Scores are computed transposed, S^T = K
@@ -351,8 +350,69 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
     }
 }
 
+// Joins the shared tiles: a workgroup per slot, the i-th of a tile's P parts taking the
+// i-th of P ranges of its rows, so that the parts' rows are spread over as many.  D / 4
+// lanes per row; where a range has fewer rows than there are such groups of lanes
+// (a row of hundreds of parts), several groups take a row's parts in turn and are
+// joined through LDS.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+join_rows_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
+                 const float *__restrict__ stat) {
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+    __shared__ Joined sums[GROUPS][LANES];
+    const Shared sh = shared[blockIdx.x];
+    if (sh.parts == 0) return;
+    const int r0 = (int)((int64_t)sh.rows * sh.index / sh.parts), r1 = (int)((int64_t)sh.rows * (sh.index + 1) / sh.parts);
+    const int grp = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    const int64_t w = (blockIdx.x >> 1) - sh.index;         // the piece with part 0
+    int ways = 1;
+    while (2 * ways * (r1 - r0) <= GROUPS && 2 * ways <= GROUPS) ways *= 2;
+    for (int row = r0; row < r1; row += GROUPS / ways) {    // (once, where ways > 1)
+        const int r = row + grp / ways;
+        Joined j = Joined::none();
+        if (r < r1) {
+            for (int i = grp % ways; i < sh.parts; i += 8 * ways) {
+                f32x2 s[8];
+                f32x4 o[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {               // (8 parts in flight; the last again behind it)
+                    const int k = i + u * ways < sh.parts ? i + u * ways : i;
+                    const int64_t x = (k == 0 ? 2 * w + 1 : 2 * (w + k)) * R + r;
+                    s[u] = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
+                    o[u] = *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u * ways < sh.parts) j.add(s[u].x, s[u].y, o[u], a.scale_log2);
+            }
+        }
+        if (ways > 1) {
+            sums[grp][c] = j;
+            __syncthreads();
+            if (grp % ways != 0) return;
+            for (int i = 1; i < ways; ++i) {
+                const Joined &x = sums[grp + i][c];
+                j.add(x.m, x.l, x.o, a.scale_log2);
+            }
+        }
+        if (r >= r1) continue;
+        const float inv = j.l > 0.0f ? 1.0f / j.l : 0.0f;
+        *reinterpret_cast<u32x2 *>(joined_row<D>(a, sh, r) + 4 * c) =
+            u32x2{pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv)};
+    }
+}
+
+// Workers: two to a compute unit (four at D = 64), which keep enough copies in flight, or
+// twice as many where there is a tile for each.  D = 128, 512 | 1024 workers, us with the join:
+// one token over 65537 keys 58 | 63, 64 over 9 to 8192 72 | 74, 256 over 1000 197 | 192, 256 over
+// 4000 723 | 708; D = 64, 1024 | 2048: one over 65537 32 | 40.
 template <int D, int NR>
-int workers(const SpanArgs &a) { return span_workers<16 * NR>(a, D == 64 ? 2048 : 1024); }
+int workers(const SpanArgs &a) {
+    const int64_t tiles = (a.B < a.T ? a.B : a.T) * (int64_t)a.G;
+    const int most = D == 64 ? 1024 : 512;
+    return span_workers<16 * NR>(a, tiles < 2 * most ? most : 2 * most);
+}
 
 template <int D, int NR>
 hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
@@ -362,7 +422,7 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
     few_attention_kernel<D, NR><<<n, 64, 0, stream>>>(a, s.shared, s.part, s.stat);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || n == 1 || !may_share<R>(a)) return e;
-    join_kernel<D, R><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    join_rows_kernel<D, R><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
     return hipGetLastError();
 }
 

@@ -341,72 +341,11 @@ struct Joined {
     }
 };
 
+// Where row r of a shared tile goes.
 template <int D>
-__device__ __forceinline__ void store_joined(const SpanArgs &a, const Shared &sh, int r, int c, const Joined &j) {
-    const float inv = j.l > 0.0f ? 1.0f / j.l : 0.0f;
+__device__ __forceinline__ uint16_t *joined_row(const SpanArgs &a, const Shared &sh, int r) {
     const int64_t row = sh.row0 + r, tok = row / a.group;
-    *reinterpret_cast<u32x2 *>(a.out + ((sh.q0 + tok) * a.H + sh.g * a.group + (row - tok * a.group)) * D + 4 * c) =
-        u32x2{pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv)};
-}
-
-// Joins the shared tiles: a workgroup per slot, the i-th of a tile's P parts taking the
-// i-th of P ranges of its rows, so that each reads about one part's worth.  D / 4 lanes
-// per row; where a range has fewer rows than there are such groups of lanes, several
-// groups take a row's parts in turn and are joined through LDS.
-template <int D, int R>
-__global__ void __launch_bounds__(256)
-join_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
-            const float *__restrict__ stat) {
-    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-    __shared__ Joined sums[GROUPS][LANES];
-    const Shared sh = shared[blockIdx.x];
-    if (sh.parts == 0) return;
-    const int r0 = (int)((int64_t)sh.rows * sh.index / sh.parts), r1 = (int)((int64_t)sh.rows * (sh.index + 1) / sh.parts);
-    const int grp = threadIdx.x / LANES, c = threadIdx.x % LANES;
-    const int64_t w = (blockIdx.x >> 1) - sh.index;         // the piece with part 0
-    auto slot = [&](int i) { return (i == 0 ? 2 * w + 1 : 2 * (w + i)) * R; };
-    int ways = 1;
-    while (2 * ways * (r1 - r0) <= GROUPS && 2 * ways <= GROUPS) ways *= 2;
-    if (ways > 1) {
-        const int r = r0 + grp / ways;
-        Joined j = Joined::none();
-        if (r < r1) {
-#pragma unroll 16
-            for (int i = grp % ways; i < sh.parts; i += ways) {
-                const int64_t x = slot(i) + r;
-                const f32x2 s = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
-                j.add(s.x, s.y, *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c), a.scale_log2);
-            }
-        }
-        sums[grp][c] = j;
-        __syncthreads();
-        if (r >= r1 || grp % ways != 0) return;
-        for (int i = 1; i < ways; ++i) {
-            const Joined &x = sums[grp + i][c];
-            j.add(x.m, x.l, x.o, a.scale_log2);
-        }
-        store_joined<D>(a, sh, r, c, j);
-        return;
-    }
-    for (int r = r0 + grp; r < r1; r += 4 * GROUPS) {
-        Joined j[4] = {Joined::none(), Joined::none(), Joined::none(), Joined::none()};
-#pragma unroll 2
-        for (int i = 0; i < sh.parts; ++i) {
-            f32x2 s[4];
-            f32x4 o[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t x = slot(i) + (r + u * GROUPS < r1 ? r + u * GROUPS : r);
-                s[u] = *reinterpret_cast<const f32x2 *>(stat + 2 * x);
-                o[u] = *reinterpret_cast<const f32x4 *>(part + x * D + 4 * c);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) j[u].add(s[u].x, s[u].y, o[u], a.scale_log2);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (r + u * GROUPS < r1) store_joined<D>(a, sh, r + u * GROUPS, c, j[u]);
-    }
+    return a.out + ((sh.q0 + tok) * a.H + sh.g * a.group + (row - tok * a.group)) * D;
 }
 
 }  // namespace svdq
