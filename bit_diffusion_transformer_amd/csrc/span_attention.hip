@@ -451,9 +451,10 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int D, bool PAGED>
+template <int D>
 hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
-    return wide(a) ? launch<D, PAGED, 8>(a, ws, stream) : launch<D, PAGED, 4>(a, ws, stream);
+    if (a.kv_len) return launch<D, true, 8>(a, ws, stream);
+    return wide(a) ? launch<D, false, 8>(a, ws, stream) : launch<D, false, 4>(a, ws, stream);
 }
 
 }  // namespace span
@@ -461,9 +462,7 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
 size_t span_tile_workspace(const SpanArgs &a) { return a.D == 64 ? span::bytes<64>(a) : span::bytes<128>(a); }
 
 hipError_t launch_span_tiles(const SpanArgs &a, void *ws, hipStream_t stream) {
-    if (a.kv_len)
-        return a.D == 64 ? span::launch<64, true>(a, ws, stream) : span::launch<128, true>(a, ws, stream);
-    return a.D == 64 ? span::launch<64, false>(a, ws, stream) : span::launch<128, false>(a, ws, stream);
+    return a.D == 64 ? span::launch<64>(a, ws, stream) : span::launch<128>(a, ws, stream);
 }
 
 }  // namespace svdq

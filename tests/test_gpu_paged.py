@@ -81,6 +81,8 @@ PACKED = [
     (7, 1, 128, [100, 1, 257]), (12, 4, 64, [511, 0, 0, 513]), (16, 1, 128, [33, 34]),
     (64, 1, 64, [9, 40]), (24, 8, 128, [640, 1000]), (10, 2, 64, [1500]), (4, 2, 128, [3001]),
     (3, 1, 128, [200, 1] * 40), (2, 2, 64, [5] * 130 + [700]), (8, 2, 128, [0, 0, 2048, 0]),
+    # many pairs of a row and a key: tiles of 256 rows
+    (32, 8, 128, [3000]), (32, 4, 64, [2999]), (40, 8, 128, [2500, 0, 1900, 900]), (48, 48, 64, [285] * 70 + [3]),
 ]
 
 
@@ -233,6 +235,34 @@ def test_lengths_past_the_table_and_starts_out_of_order():
     buf.fill_(-777.0)
     bdt.paged_attention(q, kc, vc, full, ints([2, 5, 2 ** 31 - 1]), ints([0, 48]), out=buf)
     assert bool((buf[:2] == -777).all()) and bool((buf[2:] == 0).all())
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_drawn_shapes(seed):
+    """Heads, lengths, pages and strides at random, over the cache and packed."""
+    rng = np.random.default_rng(seed)
+    G = int(rng.choice([1, 2, 3, 5, 8]))
+    H, D = G * int(rng.choice([1, 2, 3, 4, 7, 16])), int(rng.choice([64, 128]))
+    B, page = int(rng.integers(1, 90 if seed % 4 == 0 else 8)), int(rng.choice([16, 32, 64, 128, 256]))
+    causal, most = bool(rng.integers(2)), int(rng.choice([1, 3, 40, 300]))
+    new = rng.integers(0 if B > 1 else 1, most + 1, B).tolist()
+    if sum(new) == 0:
+        new[0] = 1
+    lens = [int(n + rng.integers(0, 1 + int(rng.choice([1, 100, 2000])))) for n in new]
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, new, lens, 100 + seed)
+    at = starts_of(new)
+    outs = [bdt.paged_attention(q, kc, vc, tables, ints(at), ints(lens), max_new=m, causal=causal)
+            for m in (max(max(new), 1), 4000)]
+    wide = normal(seed, sum(new), H * D + 8 * int(rng.integers(1, 5)))       # rows that lie apart
+    wide[:, :H * D] = q.view(sum(new), H * D)
+    k, v = torch.cat(ks), torch.cat(vs)
+    outs.append(bdt.packed_attention(wide[:, :H * D].unflatten(1, (H, D)), k, v, ints(at), ints(starts_of(lens)),
+                                     causal=causal))
+    for b in range(B):
+        x = slice(at[b], at[b + 1])
+        ref, tol = sequence_64(q[x], ks[b], vs[b], D ** -0.5, causal)
+        for out, what in zip(outs, ("for its most", "in tiles", "packed")):
+            check(out[x], ref, tol, "request %d, %s" % (b, what))
 
 
 # ------------------------------------------------------------------ values
