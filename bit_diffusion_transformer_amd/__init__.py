@@ -322,8 +322,8 @@ def cached_attention(X, qkv: dict, out: dict, heads: int, kv_heads: int, head_di
     svdq_paged_attention and svdq_linear.  X bf16 [T, K]: the new tokens of all requests; the qkv
     layer has (heads + 2 kv_heads) head_dim channels; the caches get the new keys and values.
     q_starts, kv_len, slots and positions from page_tables; the other arguments as for
-    qkv_norm_rope_cache and paged_attention.  Rows of no request are unspecified.  Every tensor is
-    checked first."""
+    qkv_norm_rope_cache and paged_attention.  Rows of no request are unspecified.  Every tensor and
+    max_new are checked first."""
     T, K = expect(X, "X", BF16, (None, None))
     HD = heads * head_dim
     pages, _, page, _ = expect(k_cache, "k_cache", BF16, (None, kv_heads, None, head_dim))
@@ -342,6 +342,8 @@ def cached_attention(X, qkv: dict, out: dict, heads: int, kv_heads: int, head_di
         if g is not None:
             expect(g, what, BF16, (head_dim,))
             tensors[what] = g
+    if max_new is not None and max_new < 1:
+        raise ValueError("max_new: expected at least 1, got %d" % max_new)
     one = len({t.get_device() for t in tensors.values()}) == 1
     dev = one_device(X=X) if one else one_device(**tensors)     # the latter raises
     with on(dev):

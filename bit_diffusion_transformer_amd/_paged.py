@@ -109,7 +109,7 @@ def _out(out: Optional[torch.Tensor], q: torch.Tensor, what: str = "out") -> tor
 
 
 def _scale(scale: Optional[float], D: int) -> float:
-    return D ** -0.5 if scale is None else scale
+    return max(D, 1) ** -0.5 if scale is None else scale
 
 
 def _max_new(max_new, tokens: int) -> int:

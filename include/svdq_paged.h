@@ -78,8 +78,9 @@ size_t svdq_packed_attention_workspace_bytes(const svdq_packed_shape *shape);
  * and sum; its weights are rounded once to bf16 for the product with v; one
  * rounding of the result to bf16.  A key that a row does not see takes no part
  * in it, whatever it holds.  A NaN or an infinity in a query row gives a row of
- * NaN, a NaN in a key NaN in the rows that see it, a v that is not finite an
- * infinity or NaN in its column of the rows that see it.
+ * NaN if the row sees a key, a NaN in a key NaN in the rows that see it (an
+ * infinity likewise, or no weight where its score is minus infinity), a v that is
+ * not finite an infinity or NaN in its column of the rows that see it.
  */
 int32_t svdq_packed_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                               const int32_t *q_starts, const int32_t *k_starts,
@@ -153,7 +154,8 @@ typedef struct svdq_table_shape {
  *   positions  device int32 [T] (out): the token's place in its request,
  *              cached[b] + i; -1 behind the last request
  *   counts     device int32 [2] (out): pages taken from free_pages (as many as
- *              are needed, whether there are so many or not); new tokens without
+ *              are needed, whether there are so many or not, 2^31 - 1 at most,
+ *              and no more entries are written); new tokens without
  *              a slot, those past T included.  The step can be used if the
  *              second is 0.
  * The result depends on cached, added, free_pages and the table entries of the

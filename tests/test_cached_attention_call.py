@@ -53,6 +53,12 @@ def test_tensors_that_are_not_on_a_gpu_are_refused(nothing_launched):
         bdt.cached_attention(**_args())
 
 
+@pytest.mark.parametrize("most", [0, -1])
+def test_a_most_below_one_is_refused(nothing_launched, most):
+    with pytest.raises(ValueError, match="max_new"):
+        bdt.cached_attention(**_args(), max_new=most)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["X", "cos_t", "gamma_q", "k_cache", "tables", "kv_len", "slots", "qkv", "out"])
 def test_a_tensor_left_on_the_host_is_refused(nothing_launched, name):

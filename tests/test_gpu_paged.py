@@ -176,6 +176,8 @@ PAGED = [
     (5, 5, 64, 16, [129], [3000]), (64, 1, 128, 16, [1, 3], [700, 4]), (3, 1, 128, 64, [1] * 70, list(range(1, 140, 2))),
     (8, 8, 128, 64, [5, 5], [3, 5]), (24, 24, 64, 64, [1], [20000]), (10, 2, 128, 32, [16, 7], [2222, 4444]),
     (16, 2, 128, 128, [2, 4, 1], [9000, 31, 12000]),
+    # a tile for each of twice the workers
+    (8, 8, 128, 32, [1] * 130, list(range(1, 651, 5))), (12, 6, 64, 16, [1, 2, 0, 1, 1] * 69, [7, 300, 20, 1, 99] * 69),
 ]
 
 
@@ -314,6 +316,31 @@ def test_a_query_that_is_not_finite(bad, new, lens):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("new", [[3, 1], [40, 1]])
+def test_a_query_that_is_not_finite_and_sees_no_key(new):
+    q, kc, vc, tables, _, _ = paged_inputs(4, 2, 64, 16, new, [2, 1], 3)
+    q[0] = float("nan")
+    out = bdt.paged_attention(q, kc, vc, tables, ints(starts_of(new)), ints([2, 1]), max_new=max(new))
+    assert bool((out[0] == 0).all()) and bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_a_key_that_is_infinite(new):
+    """No weight where the score is minus infinity, NaN elsewhere."""
+    n, D = 2000, 64
+    q, kc, vc, tables, ks, vs = paged_inputs(1, 1, D, 16, [new], [n], 3)
+    q[:, 0, 0] = q[:, 0, 0].abs() + 0.1
+    kc[tables[0, 3], 0, 5, 0] = -float("inf")                  # key 53
+    dead = torch.zeros(n, dtype=torch.bool, device=DEV)
+    dead[53] = True
+    args = (kc, vc, tables, ints([0, new]), ints([n]))
+    out = bdt.paged_attention(q, *args, max_new=new)
+    ref, tol = sequence_64(q, ks[0], vs[0], D ** -0.5, True, dead)
+    check(out, ref, tol, "minus infinity")
+    kc[tables[0, 3], 0, 5, 0] = float("inf")
+    assert bool(bdt.paged_attention(q, *args, max_new=new).isnan().all())
+
+
 def test_outputs_and_workspace_stay_inside():
     for H, G, D, new, lens in ((4, 2, 128, [1, 1], [3000, 500]), (6, 2, 64, [150, 3], [1000, 40])):
         q, kc, vc, tables, _, _ = paged_inputs(H, G, D, 64, new, lens, 2)
@@ -368,6 +395,34 @@ def test_in_a_graph_and_on_two_streams(new):
         assert torch.equal(out, eager), "replay %d" % it
         if it < 3:
             assert torch.equal(out, want[it % 2])
+
+
+def test_packed_in_a_graph_and_on_two_streams():
+    """Two graphs of packed calls, replayed on two streams at once."""
+    sets = [(normal(s, 700, 6, 64), normal(s + 1, 700, 2, 64), normal(s + 2, 700, 2, 64)) for s in (1, 5)]
+    at = ints([0, 600, 600, 690])
+    want = [bdt.packed_attention(*s, at) for s in sets]
+    torch.cuda.synchronize()
+    streams, graphs, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for s in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(bdt.packed_attention(*s, at, out=torch.full_like(s[0], -3.0)))
+    for _ in range(4):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for s, o, w in zip(sets, outs, want):
+            assert torch.equal(o[:690], w[:690]) and bool((o[690:] == -3).all())
+            assert torch.equal(bdt.packed_attention(*s, at)[:690], w[:690])
+            o[:690].fill_(0)
+
+
+def test_no_columns():
+    x = torch.empty(3, 4, 0, dtype=BF, device=DEV)
+    with pytest.raises(RuntimeError, match="head_dim"):
+        bdt.packed_attention(x, x, x, ints([0, 3]))
 
 
 def test_offsets_past_32_bits():
