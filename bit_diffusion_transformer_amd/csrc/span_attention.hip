@@ -19,16 +19,18 @@ namespace span {
 
 using namespace attn;
 
-template <int D, int WAVES>
+template <int D, bool PAGED, int WAVES>
 struct Lds {
     static constexpr int TILE = kKeys * D * 2;     // bytes of a K or V block
-    uint8_t k[2][TILE];
-    uint8_t v[2][TILE];
-    Seq seqs[WAVES][64];                                // a wave each: they are not in step
+    static constexpr int OWN = 32 * D * 2;         // of a narrow tile's unit, a wave's own
+    static constexpr int BYTES = PAGED && 2 * WAVES * OWN > 4 * TILE ? 2 * WAVES * OWN : 4 * TILE;
+    uint8_t kv[BYTES];                             // K [2], V [2]; narrow: a wave's K and V, wave after wave
+    Seq seqs[WAVES][64];                           // a wave each: they are not in step
+    f32x2 stat[PAGED ? WAVES : 1][32];             // narrow: maximum and sum of each wave's rows
 };
 
 template <int D, bool PAGED, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, D == 64 ? 4 : 2)
+__global__ void __launch_bounds__(64 * WAVES, 2)
 span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict__ part,
                       float *__restrict__ stat) {
     constexpr int kRows = 32 * WAVES;
@@ -36,7 +38,9 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     constexpr int RPT = 512 / D;                   // rows per 1 KB copy
     constexpr int SEGS = D / 8;                    // 16-byte segments of a row
     constexpr int PART = kKeys / WAVES, COPIES = PART / RPT;   // rows and copies per wave
-    __shared__ __align__(1024) Lds<D, WAVES> lds;
+    typedef Lds<D, PAGED, WAVES> L;
+    __shared__ __align__(1024) L lds;
+    uint8_t *const lds_v0 = lds.kv + 2 * L::TILE;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5, col = lane & 31;
 
@@ -63,15 +67,15 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     const uint8_t *k_rd[DK], *v_rd[DB];
 #pragma unroll
     for (int t = 0; t < DK; ++t)
-        k_rd[t] = lds.k[0] + col * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(col));
+        k_rd[t] = lds.kv + col * (D * 2) + 16 * ((2 * t + h2) ^ swz_k<D>(col));
     {
         const int i = lane & 15, row = 4 * h2 + (i >> 2);
         const int sub = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);     // segment of a 32-wide block
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-            v_rd[d] = lds.v[0] + row * (D * 2) + 16 * ((4 * d + sub) ^ swz_v<D>(row)) + 8 * (lane & 1);
+            v_rd[d] = lds_v0 + row * (D * 2) + 16 * ((4 * d + sub) ^ swz_v<D>(row)) + 8 * (lane & 1);
     }
-    const uint32_t lds_k = lds_address(lds.k) + wave * COPIES * 1024, lds_v = lds_address(lds.v) + wave * COPIES * 1024;
+    const uint32_t lds_k = lds_address(lds.kv) + wave * COPIES * 1024, lds_v = lds_k + 2 * L::TILE;
     const float scale_log2 = a.scale_log2;
 
     for (;; ) {
@@ -82,7 +86,8 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         const int rows = rows_left < kRows ? (int)rows_left : kRows;
         const int tok0 = token_of(a, (double)row0), rem0 = (int)(row0 - (int64_t)tok0 * a.group);
         const int nk = at.s.nk;
-        const int mine = 32 * wave + col;
+        const bool narrow = PAGED && Place<kRows>::narrow(a, at.s);
+        const int mine = narrow ? col : 32 * wave + col;
         const bool active = 32 * wave < rows;      // uniform over the wave
         const int row = mine < rows ? mine : rows - 1;   // rows past the last: never stored
         const int ahead = token_of(a, rem0 + row), tok = tok0 + ahead, sub = rem0 + row - ahead * a.group;
@@ -132,7 +137,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 k0 = kb + n0 * k_row;
                 v0 = vb + n0 * v_row;
             }
-            const uint32_t kd = lds_k + BUF * Lds<D, WAVES>::TILE, vd = lds_v + BUF * Lds<D, WAVES>::TILE;
+            const uint32_t kd = lds_k + BUF * L::TILE, vd = lds_v + BUF * L::TILE;
             if (__builtin_expect(left >= PART, 1)) {
                 copies_in_flight(k0, k_at, kd);
                 copies_in_flight(v0, v_at, vd);
@@ -143,10 +148,59 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                         copy_in_flight(k0, k_at[c], kd + c * 1024);
                         copy_in_flight(v0, v_at[c], vd + c * 1024);
                     } else {
-                        *reinterpret_cast<u32x4 *>(lds.v[BUF] + (wave * COPIES + c) * 1024 + lane * 16) = u32x4{};
+                        *reinterpret_cast<u32x4 *>(lds_v0 + BUF * L::TILE + (wave * COPIES + c) * 1024 + lane * 16) = u32x4{};
                     }
                 }
             }
+        };
+
+        // A narrow tile: every wave has all its rows and goes over units of 32 keys of its own, the
+        // wave-th, then every WAVES-th; K and V of a unit lie in LDS of its own, K of the next one
+        // is copied as soon as the scores are there, V as soon as it has been used.
+        constexpr int NC = 16 / RPT;               // copies of 16 keys
+        const int u0 = 2 * first + wave, seen = (high + 31) / 32, u1 = 2 * last < seen ? 2 * last : seen;
+        const uint32_t own = (uint32_t)wave * (2 * L::OWN);
+        uint32_t nk_at[NC], nv_at[NC];             // bytes from the first of 16 keys
+        bool full = false, full_next = false;      // every copy of the unit was issued
+        auto issue_unit = [&](int u, auto which) __attribute__((always_inline)) {
+            constexpr bool V = decltype(which)::value;
+            const int j = (u - u0) / WAVES;
+            if (!V && (j & 31) == 0) {             // lane l: 16 keys of this wave's unit j + l / 2
+                const int n = 16 * (2 * (u + WAVES * (lane >> 1)) + (lane & 1));
+                const int p = n < nk ? table[n >> a.page_shift] : -1;
+                const bool good = p >= 0 && p < a.pages;
+                pages = good ? p : -1;
+                bad16 = __ballot(!good && n < nk);
+            }
+            if (!V) {
+                bad_next = (uint32_t)(bad16 >> (2 * (j & 31))) & 3u;
+                full_next = true;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n0 = 32 * u + 16 * h, page = __builtin_amdgcn_readlane(pages, 2 * (j & 31) + h);
+                const int left = page < 0 ? 0 : nk - n0;
+                const int64_t r = ((((int64_t)page * a.G + at.g) << a.page_shift) +
+                                   (n0 & ((1 << a.page_shift) - 1))) * (D * 2);
+                const uint32_t to = own + (V ? L::OWN : 0) + h * 16 * D * 2;
+                const uint32_t (&off)[NC] = V ? nv_at : nk_at;
+                if (__builtin_expect(left >= 16, 1)) {
+                    copies_in_flight((V ? vb : kb) + r, off, lds_address(lds.kv) + to);
+                } else {
+                    full_next = false;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (c * RPT + cp_row < left)
+                            copy_in_flight((V ? vb : kb) + r, off[c], lds_address(lds.kv) + to + c * 1024);
+                        else if (V)
+                            *reinterpret_cast<u32x4 *>(lds.kv + to + c * 1024 + lane * 16) = u32x4{};
+                }
+            }
+        };
+        auto start_units = [&]() __attribute__((always_inline)) {
+            if (u0 >= u1) return;
+            issue_unit(u0, std::false_type());
+            issue_unit(u0, std::true_type());
         };
 
         u32x4 qf[DK];
@@ -155,7 +209,17 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                                 (int64_t)(at.g * a.group + sub) * D + 8 * h2;
 #pragma unroll
             for (int s = 0; s < DK; ++s) qf[s] = *reinterpret_cast<const u32x4 *>(p + 16 * s);
-            if (first < last) issue(first, std::integral_constant<int, 0>());
+            if (narrow) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int r = c * RPT + cp_row;
+                    nk_at[c] = r * (D * 2) + 16 * (cp_slot ^ swz_k<D>(r));
+                    nv_at[c] = r * (D * 2) + 16 * (cp_slot ^ swz_v<D>(r));
+                }
+                start_units();
+            } else if (first < last) {
+                issue(first, std::integral_constant<int, 0>());
+            }
             // A row with a value that is not finite becomes a row of NaN: scores of minus
             // infinity alone would look like keys that it does not see.
             uint32_t odd = 0;
@@ -183,7 +247,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
             m = -__builtin_inff();
             l = 0.0f;
             auto block = [&](int i, auto buffer) __attribute__((always_inline)) {
-                constexpr int BUF = decltype(buffer)::value, AT = BUF * Lds<D, WAVES>::TILE;
+                constexpr int BUF = decltype(buffer)::value, AT = BUF * L::TILE;
                 const int n0 = i * kKeys;
                 wait_loads<0>();
                 wave_barrier_all();
@@ -331,6 +395,152 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                 if (i + 1 < last) block(i + 1, std::integral_constant<int, 1>());
             }
         };
+        if (PAGED && narrow) {
+            auto units = [&](auto mode) __attribute__((always_inline)) {
+                constexpr bool careful = decltype(mode)::value;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+                m = -__builtin_inff();
+                l = 0.0f;
+                for (int u = u0; u < u1; u += WAVES) {
+                    const int n0 = 32 * u;
+                    bad = bad_next;
+                    full = full_next;
+                    if (full)
+                        wait_loads<2 * NC>();      // all but this unit's V
+                    else
+                        wait_loads<0>();
+                    asm volatile("" ::: "memory");
+                    f32x16 s = {};
+#pragma unroll
+                    for (int t = 0; t < DK; ++t)
+                        s = mfma_bf16_32x32x16(*reinterpret_cast<const u32x4 *>(k_rd[t] + own), qf[t], s);
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    const bool more = u + WAVES < u1;
+                    if (more) issue_unit(u + WAVES, std::false_type());
+                    const bool edge = n0 + 32 > low || bad != 0;
+                    if (edge) {
+                        masked = true;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int n = n0 + 8 * (e / 4) + 4 * h2 + e % 4;
+                            if (n >= limit || (bad >> (e / 8) & 1)) s[e] = -__builtin_inff();
+                        }
+                    }
+                    float top = s[0];
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+                    top = max_both_halves(top);
+                    if (__any((top - m) * scale_log2 > 8.0f)) {
+                        const float m1 = fmaxf(m, top);
+                        const float f = m == m1 ? 1.0f : __builtin_amdgcn_exp2f((m - m1) * scale_log2);
+                        m = m1;
+                        l *= f;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[d][e] *= f;
+                    }
+                    float off = m * scale_log2;
+                    const bool far = fabsf(off) > 1024.0f;
+                    if (__any(far)) {
+                        const float by = far && m > -__builtin_inff() ? m : 0.0f;
+                        off = far ? 0.0f : off;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[e] -= by;
+                    }
+                    u32x4 p[2];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], scale_log2, -off));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            p[t][x] = pack_bf16x2(s[8 * t + 2 * x], s[8 * t + 2 * x + 1]);
+                            l = add_pair(p[t][x], l);
+                        }
+                    if (more && full_next)
+                        wait_loads<2 * NC>();      // all but the next unit's K
+                    else
+                        wait_loads<0>();
+                    asm volatile("" ::: "memory");
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            u32x4 x, odd = {};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const u32x2 y = read_transposed(v_rd[d] + own + L::OWN - 2 * L::TILE + (16 * t + 8 * h) * (D * 2));
+                                x[2 * h] = y.x;
+                                x[2 * h + 1] = y.y;
+                            }
+                            if (careful && edge)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t f = not_finite(x[j]);
+                                    odd[j] = (f >> 15) * 0x3F80u;
+                                    x[j] &= ~((f >> 15) * 0xFFFFu);
+                                }
+                            o[d] = mfma_bf16_32x32x16(x, p[t], o[d]);
+                            if (careful && edge) {
+                                const f32x16 c = mfma_bf16_32x32x16(odd, p[t], f32x16{});
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (c[e] > 0.0f) o[d][e] = __builtin_nanf("");
+                            }
+                        }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    if (more) issue_unit(u + WAVES, std::true_type());
+                }
+            };
+            units(std::false_type());
+            float z = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z = __builtin_fmaf(o[d][e], 0.0f, z);
+            if (__builtin_expect(__any(masked && z != z), 0)) {
+                start_units();
+                units(std::true_type());
+            }
+            // The waves' results, each in its own LDS, then their sums, four columns at a time.
+            l = sum_both_halves(l);
+            f32x4 *const mine_o = reinterpret_cast<f32x4 *>(lds.kv + own) + lane;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mine_o[64 * (4 * d + e)] = f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+            if (h2 == 0) lds.stat[wave][col] = f32x2{m, l};
+            const int slot = share(piece, row0, rows, shared);
+            __syncthreads();
+            for (int i = wave; i < 4 * DB; i += WAVES) {
+                Joined sum = Joined::none();
+#pragma unroll
+                for (int x = 0; x < WAVES; ++x) {
+                    const f32x2 s = lds.stat[x][col];
+                    sum.add(s.x, s.y, reinterpret_cast<const f32x4 *>(lds.kv + x * (2 * L::OWN))[64 * i + lane], scale_log2);
+                }
+                if (slot >= 0) {
+                    *reinterpret_cast<f32x4 *>(part + (int64_t)slot * WAVES * (32 * D) + 256 * i + 4 * lane) = sum.o;
+                    if (i == 0 && h2 == 0) {
+                        const int64_t r = (int64_t)slot * kRows + col;
+                        stat[2 * r] = sum.m;
+                        stat[2 * r + 1] = sum.l;
+                    }
+                } else if (col < rows) {
+                    const float inv = sum.l > 0.0f ? 1.0f / sum.l : 0.0f;
+                    *reinterpret_cast<u32x2 *>(a.out + ((int64_t)(at.s.q0 + tok) * a.H + at.g * a.group + sub) * D +
+                                               8 * i + 4 * h2) =
+                        u32x2{pack_bf16x2(sum.o.x * inv, sum.o.y * inv), pack_bf16x2(sum.o.z * inv, sum.o.w * inv)};
+                }
+            }
+            __syncthreads();
+            if (!piece.next(a)) return;
+            continue;
+        }
         pass(std::false_type());
         float z = 0.0f;                            // NaN where something is not finite
 #pragma unroll
@@ -421,7 +631,7 @@ join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__
 // Workers: as many workgroups as the compute units hold at once, two waves to a SIMD (four
 // at D = 64), or fewer where even the most keys that the shape allows make fewer pieces.
 template <int D, int WAVES>
-int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, (D == 64 ? 4096 : 2048) / WAVES); }
+int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, 2048 / WAVES); }
 
 // Tiles of 256 rows read K and V half as often as tiles of 128, and fill less well.  With many
 // pairs of a row and a key (half of them seen with `causal`), and over a cache, 256.  128 | 256 us,

@@ -34,6 +34,9 @@ constexpr int kTileCost = R < 128 ? 128 : 256;
 template <int R>
 constexpr int kLeast = R < 128 ? 2 : 4;
 
+constexpr double kNarrow = 0.25;       // a key's length in a narrow tile
+constexpr int kNarrowCost = 512;
+
 struct Seq {
     int q0, nq, k0, nk;            // first row and rows of q, of k
 };
@@ -113,7 +116,12 @@ struct Place {
     __device__ static __forceinline__ double tiles(const SpanArgs &a, const Seq &v) {
         return floor(((double)v.nq * a.group + (R - 1)) * (1.0 / R));
     }
+    // A paged sequence of one wave's rows in a wide tile: the waves divide its keys.
+    __device__ static __forceinline__ bool narrow(const SpanArgs &a, const Seq &v) {
+        return R > 32 && a.kv_len && (int64_t)v.nq * a.group <= 32;
+    }
     __device__ static __forceinline__ double cost0(const SpanArgs &a, const Seq &v) {
+        if (narrow(a, v)) return (v.nk * kNarrow + kNarrowCost) * a.group;
         const int less = a.causal ? v.nq : 0;
         return ((double)(v.nk > less ? v.nk - less : 0) + kTileCost<R>) * a.group + step(a);
     }
