@@ -633,13 +633,17 @@ join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__
 template <int D, int WAVES>
 int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, 2048 / WAVES); }
 
-// Tiles of 256 rows read K and V half as often as tiles of 128, and fill less well.  With many
-// pairs of a row and a key (half of them seen with `causal`), and over a cache, 256.  128 | 256 us,
-// D = 128: 32 heads on 8, causal, one prompt of 1000 39.8 | 43.5, 2000 67 | 68, 4000 174 | 171,
-// 8000 530 | 515; twelve of 1 to 2000 103 | 107; 24 heads, four images of 777 to 4096 342 | 317.
-// Paged, 12 heads, 2 x 1560 rows over 32760 734 | 677; 512 over 4608 64.3 | 64.9.
+// Tiles of 256 rows read K and V half as often as tiles of 128, and fill less well.  128 | 256, us:
+// Packed, with many pairs of a row and a key (half of them seen with `causal`), 256.  D = 128: 32
+// heads on 8, causal, one prompt of 1000 39.8 | 43.5, 2000 67 | 68, 4000 174 | 171, 8000 530 | 515;
+// twelve of 1 to 2000 103 | 107; 24 heads, four images of 777 to 4096 342 | 317.
+// Paged, where the call does not know how many keys there are, with many rows.  D = 128: 12 heads,
+// 2 x 1560 rows over 32760 734 | 677; 32 heads on 8, 40 over 4000 28.0 | 31.2, 512 over 4608 65.9 |
+// 65.9, 48 decoding requests and 1000 new 82 | 78; D = 64: 28 heads on 4, 512 over 4608 beside
+// 31 decoding requests 46 | 49, 48 decoding and 1000 new 31 | 37; 12 heads, 2 x 1560 over 32760
+// 425 | 406; 32 on 4, 2048 over 20000 406 | 373.
 bool wide(const SpanArgs &a) {
-    if (a.max_new > 0) return true;
+    if (a.max_new > 0) return (double)a.T * a.H * a.D >= 0x1p21;
     const double pairs = (double)a.T * (double)a.Tk / a.B * a.H;
     return pairs >= (a.causal ? 0x1p28 : 0x1p27);
 }
@@ -663,7 +667,7 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
 
 template <int D>
 hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
-    if (a.kv_len) return launch<D, true, 8>(a, ws, stream);
+    if (a.kv_len) return wide(a) ? launch<D, true, 8>(a, ws, stream) : launch<D, true, 4>(a, ws, stream);
     return wide(a) ? launch<D, false, 8>(a, ws, stream) : launch<D, false, 4>(a, ws, stream);
 }
 

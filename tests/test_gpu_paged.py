@@ -176,6 +176,10 @@ PAGED = [
     (5, 5, 64, 16, [129], [3000]), (64, 1, 128, 16, [1, 3], [700, 4]), (3, 1, 128, 64, [1] * 70, list(range(1, 140, 2))),
     (8, 8, 128, 64, [5, 5], [3, 5]), (24, 24, 64, 64, [1], [20000]), (10, 2, 128, 32, [16, 7], [2222, 4444]),
     (16, 2, 128, 128, [2, 4, 1], [9000, 31, 12000]),
+    # many rows: tiles of 256 rows, and requests of few rows beside them
+    (32, 8, 128, 64, [1] * 20 + [600] + [2, 8, 9, 0], list(range(1, 4000, 200)) + [1700, 900, 8, 9, 77]),
+    (28, 4, 64, 32, [4, 1200, 1, 5], [3333, 1200, 5000, 1]), (24, 24, 128, 256, [32, 800, 33], [1000, 801, 600]),
+    (20, 1, 64, 16, [1, 1, 2, 1700], [7000, 300, 90, 1750]),
     # a tile for each of twice the workers
     (8, 8, 128, 32, [1] * 130, list(range(1, 651, 5))), (12, 6, 64, 16, [1, 2, 0, 1, 1] * 69, [7, 300, 20, 1, 99] * 69),
 ]
@@ -300,6 +304,26 @@ def test_later_keys_that_are_not_finite_stay_out_of_earlier_rows(H, G, D, lens, 
     other = [d for d in range(D) if d != 3]
     assert torch.equal(out[n:][..., other], clean[n:][..., other])
     assert not bool(torch.isfinite(out[n:, :, 3]).any())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H,G,D,new,lens", [(8, 2, 128, [5, 200, 8], [1000, 300, 40]), (8, 2, 64, [5, 200, 8], [1000, 300, 40]),
+                                            (32, 8, 128, [3, 600, 8], [5000, 700, 9]), (12, 2, 64, [2, 5], [3000, 5])])
+def test_later_values_of_a_cache_stay_out_of_earlier_rows(H, G, D, new, lens, bad):
+    """The last key of each request, which only its last token sees."""
+    page = 32
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, new, lens, 4)
+    at, kv = starts_of(new), ints(lens)
+    clean = bdt.paged_attention(q, kc, vc, tables, ints(at), kv, max_new=max(new))
+    for b, n in enumerate(lens):
+        vc[tables[b, (n - 1) // page], :, (n - 1) % page, 3] = bad
+    out = bdt.paged_attention(q, kc, vc, tables, ints(at), kv, max_new=max(new))
+    last = torch.zeros(sum(new), dtype=torch.bool, device=DEV)
+    last[[x - 1 for x in at[1:]]] = True
+    assert torch.equal(out[~last], clean[~last])
+    assert not bool(torch.isfinite(out[last][..., 3]).any())
+    other = [d for d in range(D) if d != 3]
+    assert torch.equal(out[last][..., other], clean[last][..., other])
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
