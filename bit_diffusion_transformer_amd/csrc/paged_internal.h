@@ -27,7 +27,7 @@ struct SpanArgs {
     double inv_group;
 };
 
-// Tiles of 128 rows; paged with at most 32 rows of a request and key head: a wave each.
+// Tiles of 128 or 256 rows; paged with at most 32 rows of a request and key head: a wave each.
 size_t span_tile_workspace(const SpanArgs &a);
 hipError_t launch_span_tiles(const SpanArgs &a, void *ws, hipStream_t stream);
 size_t span_few_workspace(const SpanArgs &a);
