@@ -15,7 +15,9 @@
 // point (exact; a 64-bit integer product or quotient takes many times as long, and
 // a short call is mostly this): tile t of a sequence is c0 + S t long (S = R with
 // `causal`: R rows are R / group tokens, so many more keys; S = 0 without).  Cuts
-// are anywhere, but every worker computes them in the same way.
+// are anywhere, but every worker computes them in the same way.  More than 64 sequences
+// are measured in 64 ranges, a lane each, and searched in two levels: 2048 requests over 100
+// keys, 8 heads on 2 of 128, 47 us (59 in chunks of 64), 8192 213 (286).
 #pragma once
 
 #include "paged_internal.h"
@@ -163,15 +165,42 @@ struct Place {
         }
         nb = (keys + kKeys - 1) / kKeys;
     }
-    // The tile that holds position x (0 <= x < G head); sum: load_chunk's of the first chunk,
-    // where there is only one.
+    // The line of one key head -> its length; -> the sums up to this lane's sequence or, where
+    // there are more than 64, up to the end of its range of them.
+    __device__ static __forceinline__ int range_of(const SpanArgs &a) { return (a.B + 63) >> 6; }
+    __device__ __forceinline__ double measure(const SpanArgs &a) {
+        double sum;
+        if (a.B <= 64) {
+            sum = load_chunk(a, 0);
+        } else {
+            const int range = range_of(a), b0 = (threadIdx.x & 63) * range;
+            sum = 0.0;
+#pragma unroll 4
+            for (int i = 0; i < range; ++i) {
+                if (b0 + i >= a.B) break;
+                const Seq v = load_seq(a, b0 + i);
+                sum += before(a, cost0(a, v), tiles(a, v));
+            }
+            sum = scan(sum);
+        }
+        head = lane_of(sum, 63);
+        return sum;
+    }
+    // The tile that holds position x (0 <= x < G head); sum: measure's.
     __device__ __forceinline__ void find(const SpanArgs &a, double sum, double x) {
         g = uniform((int)(x * __builtin_amdgcn_rcp(head)));
         while (g > 0 && g * head > x) --g;
         while (g + 1 < a.G && (g + 1) * head <= x) ++g;
         double base = g * head;
         b = a.B - 1;
-        for (int b0 = 0;; b0 += 64) {
+        int b0 = 0;
+        if (a.B > 64) {
+            const uint64_t past = __ballot(base + sum > x);
+            const int l = past ? __builtin_ctzll(past) : 63;
+            if (l > 0) base += lane_of(sum, l - 1);
+            b0 = l * range_of(a);
+        }
+        for (;; b0 += 64) {
             if (a.B > 64) sum = load_chunk(a, b0);
             const uint64_t past = __ballot(base + sum > x);
             if (past) {
@@ -236,12 +265,7 @@ struct Piece {
     __device__ __forceinline__ bool open(const SpanArgs &a, Seq *lds, int worker, int most) {
         w = worker;
         at.seqs = lds;
-        double sum = at.load_chunk(a, 0);
-        at.head = lane_of(sum, 63);
-        for (int b0 = 64; b0 < a.B; b0 += 64) {
-            sum = at.load_chunk(a, b0);
-            at.head += lane_of(sum, 63);
-        }
+        const double sum = at.measure(a);
         total = uniform(at.head * a.G);
         if (!(total > 0.0)) return false;
         const double n = total * a.inv_group * (1.0 / (kLeast<R> * kKeys));

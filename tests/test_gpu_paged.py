@@ -100,6 +100,29 @@ def test_packed_attention(H, G, D, lens, causal):
     assert torch.equal(bdt.packed_attention(q, k, v, ints(at), causal=causal), out)
 
 
+@pytest.mark.parametrize("B", [65, 4096, 4097, 9000])
+def test_many_sequences(B):
+    """Against the same rows as equal sequences of one batched form."""
+    H, G, D, n = 3, 1, 64, 5
+    T = B * n
+    q, k, v = normal(1, T, H, D), normal(2, T, G, D), normal(3, T, G, D)
+    out = bdt.packed_attention(q, k, v, ints([n * i for i in range(B + 1)]))
+    x, y, z = (t.view(B, n, -1, D).double().transpose(1, 2) for t in (q, k, v))
+    s = D ** -0.5 * (x @ y.transpose(-1, -2).contiguous())
+    s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1), -float("inf"))
+    p = torch.softmax(s, -1)
+    ref, w = p @ z, p @ z.abs()
+    d = (D + 8) * 2.0 ** -23 * D ** -0.5 * (x.abs() @ y.abs().transpose(-1, -2).contiguous()).amax(-1, keepdim=True)
+    tol = 2.0 ** -8 * ref.abs() + w * (2 * d + 2.0 ** -8 + 2 * n * 2.0 ** -23 + 2.0 ** -12)
+    check(out, ref.transpose(1, 2).reshape(T, H, D), tol.transpose(1, 2).reshape(T, H, D), "%d sequences" % B)
+    # every second one empty, its rows left to its neighbour
+    at = [n * (i - i % 2) for i in range(B)] + [T]
+    got = bdt.packed_attention(q, k, v, ints(at), causal=False)
+    for b in (0, 1, 2, 63, 64, B // 2, B - 2, B - 1):
+        r = slice(at[b], at[b + 1])
+        check(got[r], *sequence_64(q[r], k[r], v[r], D ** -0.5, False), "sequence %d of %d" % (b, B))
+
+
 @pytest.mark.parametrize("H,G,D,lens,keys", [
     (2, 1, 128, [3, 1, 70], [500, 0, 70]), (4, 4, 64, [1], [4000]), (6, 2, 128, [130, 5], [64, 3000]),
     (8, 2, 128, [1, 1, 1, 200], [1, 0, 2000, 199]), (2, 2, 64, [300], [10]),
