@@ -609,9 +609,15 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
 
 // Joins the shared tiles: a workgroup per slot.  A tile is WAVES x D / 32 items of 32 rows
 // and 32 columns, of which the i-th of P parts takes the i-th of P ranges; 128 threads
-// an item, which read whole kilobytes of a part as its wave wrote them.
+// an item, which read whole kilobytes of a part as its wave wrote them.  Tiles of 256 rows,
+// which seldom have many parts: four items at once, since an item's loads wait for the one
+// before (57 MB 15.4 us; two at once 18.5, eight 15.4).  Tiles of 128: two (9.6 us, as four) and
+// four parts at once: tiles of 64 parts take 41 us with their attention, 48 one at a time.
+template <int WAVES>
+constexpr int kJoinThreads = 64 * WAVES;
+
 template <int D, int WAVES>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads<WAVES>)
 join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__restrict__ part,
                   const float *__restrict__ stat) {
     constexpr int DB = D / 32, ITEMS = WAVES * DB;
@@ -620,7 +626,7 @@ join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__
     const int i0 = ITEMS * sh.index / sh.parts, i1 = ITEMS * (sh.index + 1) / sh.parts;
     const int col = threadIdx.x & 31, e = (threadIdx.x >> 5) & 3;
     const int64_t w = (blockIdx.x >> 1) - sh.index;         // the piece with part 0
-    for (int item = i0 + (threadIdx.x >> 7); item < i1; item += 2) {
+    for (int item = i0 + (threadIdx.x >> 7); item < i1; item += kJoinThreads<WAVES> / 128) {
         const int wave = item / DB, db = item % DB, r = 32 * wave + col;
         if (r >= sh.rows) continue;
         Joined lo = Joined::none(), hi = Joined::none();    // 4 columns each
@@ -672,7 +678,7 @@ hipError_t launch(const SpanArgs &a, void *ws, hipStream_t stream) {
     span_attention_kernel<D, PAGED, WAVES><<<n, 64 * WAVES, 0, stream>>>(a, s.shared, s.part, s.stat);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || n == 1 || !may_share<R>(a)) return e;
-    join_tiles_kernel<D, WAVES><<<2 * n, 256, 0, stream>>>(a, s.shared, s.part, s.stat);
+    join_tiles_kernel<D, WAVES><<<2 * n, kJoinThreads<WAVES>, 0, stream>>>(a, s.shared, s.part, s.stat);
     return hipGetLastError();
 }
 
