@@ -249,6 +249,24 @@ def test_pages_outside_the_cache_hold_no_keys(D, page, H, G, new, lens):
     assert bool((none == 0).all())
 
 
+@pytest.mark.parametrize("D,chunk", [(64, 3), (128, 1100)])
+def test_many_long_requests_in_tiles(D, chunk):
+    """So many that a workgroup has thousands of keys of one request of few rows; a page is missing."""
+    H, page, n = 16, 64, 9000
+    new, lens = [1] * 40 + [chunk], [n - 7 * b for b in range(40)] + [chunk]
+    q, kc, vc, tables, ks, vs = paged_inputs(H, H, D, page, new, lens, 8)
+    tables[1, 130] = -1
+    dead = torch.zeros(lens[1], dtype=torch.bool, device=DEV)
+    dead[130 * page:131 * page] = True
+    at = starts_of(new)
+    for most in (None, 1):
+        out = bdt.paged_attention(q, kc, vc, tables, ints(at), ints(lens), max_new=most)
+        for b in (0, 1, 2, 17, 39, 40):
+            x = slice(at[b], at[b + 1])
+            ref, tol = sequence_64(q[x], ks[b], vs[b], D ** -0.5, True, dead if b == 1 else None)
+            check(out[x], ref, tol, "request %d" % b)
+
+
 def test_lengths_past_the_table_and_starts_out_of_order():
     """Lengths are clamped to the table's width; starts are clamped, and a sequence that ends
     before it starts has no rows; rows of no sequence stay."""
