@@ -20,6 +20,10 @@ __device__ __forceinline__ float add_pair(uint32_t x, float c) {
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
+// bf16 ones in the halves of a pair of keys n, n + 1 that a row sees, the first `limit` keys.
+__device__ __forceinline__ uint32_t seen_pair(int n, int limit) {
+    return (n < limit ? 0x3F80u : 0u) | (n + 1 < limit ? 0x3F800000u : 0u);
+}
 __device__ __forceinline__ float max_both_halves(float x) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));

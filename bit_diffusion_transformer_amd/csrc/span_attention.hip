@@ -249,7 +249,8 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
         // A v that is not finite, of a key that only some rows of a block see, would reach the
         // others as zero times it.  That shows as a result that is not finite, and the part is
         // gone over once more with such values taken out of the blocks that have a mask, and a
-        // NaN put where a row gives one of them a weight.
+        // NaN put where a row sees one of them, whatever its weight: in the blocks without a
+        // mask a weight of zero gives one too.
         bool masked = false;
         auto pass = [&](auto mode) __attribute__((always_inline)) {
             constexpr bool careful = decltype(mode)::value;
@@ -369,6 +370,11 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                         if (st == 1) ps = p[0][1];
                         if (st == 2) ps = p[1][0];
                         if (st == 3) ps = p[1][1];
+                        const int lim = PAGED && (bad >> st & 1) ? 0 : limit;
+                        u32x4 seen;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            seen[x] = seen_pair(n0 + 16 * st + 8 * (x >> 1) + 4 * h2 + 2 * (x & 1), lim);
 #pragma unroll
                         for (int d = 0; d < DB; ++d) {
                             u32x4 x, odd;
@@ -385,7 +391,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                                 x[j] &= ~((f >> 15) * 0xFFFFu);
                             }
                             o[d] = mfma_bf16_32x32x16(x, ps, o[d]);
-                            const f32x16 c = mfma_bf16_32x32x16(odd, ps, f32x16{});
+                            const f32x16 c = mfma_bf16_32x32x16(odd, seen, f32x16{});
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 if (c[e] > 0.0f) o[d][e] = __builtin_nanf("");
@@ -496,7 +502,12 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
                                 }
                             o[d] = mfma_bf16_32x32x16(x, p[t], o[d]);
                             if (careful && edge) {
-                                const f32x16 c = mfma_bf16_32x32x16(odd, p[t], f32x16{});
+                                const int lim = bad >> t & 1 ? 0 : limit;
+                                u32x4 seen;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    seen[y] = seen_pair(n0 + 16 * t + 8 * (y >> 1) + 4 * h2 + 2 * (y & 1), lim);
+                                const f32x16 c = mfma_bf16_32x32x16(odd, seen, f32x16{});
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     if (c[e] > 0.0f) o[d][e] = __builtin_nanf("");

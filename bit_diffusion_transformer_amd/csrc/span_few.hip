@@ -195,8 +195,9 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
         float m[NR], l[NR];
         bool masked = false;
         // CAREFUL: once more, with values of v that are not finite taken out of the units that
-        // have a mask, and a NaN put where a row gives one of them a weight (zero times such a
-        // value would reach the rows that do not see its key).
+        // have a mask (zero times such a value would reach the rows that do not see its key),
+        // and a NaN put where a row sees one of them, whatever its weight: in the units
+        // without a mask a weight of zero gives one too.
         auto pass = [&](auto mode) __attribute__((always_inline)) {
             constexpr bool careful = decltype(mode)::value;
 #pragma unroll
@@ -241,7 +242,14 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                                 if (n >= limit[r] || (bad[BUF] >> t & 1)) s[t][r][e] = -__builtin_inff();
                         }
                 }
-                u32x4 p[NR];
+                u32x4 p[NR], seen[NR];
+                if (careful && edge)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            seen[r][x] = seen_pair(n0 + 16 * (x / 2) + 4 * g4 + 2 * (x & 1),
+                                                   bad[BUF] >> (x / 2) & 1 ? 0 : limit[r]);
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     float top = s[0][r][0];
@@ -300,7 +308,7 @@ few_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict_
                     for (int r = 0; r < NR; ++r) {
                         o[d][r] = mfma_bf16_16x16x32(vf, p[r], o[d][r]);
                         if (careful && edge) {
-                            const f32x4 c = mfma_bf16_16x16x32(odd, p[r], f32x4{});
+                            const f32x4 c = mfma_bf16_16x16x32(odd, seen[r], f32x4{});
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (c[e] > 0.0f) o[d][r][e] = __builtin_nanf("");
