@@ -18,7 +18,7 @@ import torch
 from ._binding import (ACT_GELU, ACT_NONE, EXPORTS, GROUP, LIB_PATH, SVDQError,  # noqa: F401
                        QkvEpilogue, TILES_AUTO, TILES_FULL, TILES_QUARTER, TILES_KSPLIT,
                        TILES_KSPLIT_QUARTER, qkv_epilogue,
-                       load_library, svdq_abi_version, svdq_awq_pack_weights,
+                       _check_without_workspace, load_library, svdq_abi_version, svdq_awq_pack_weights,
                        svdq_awq_packed_bytes, svdq_awq_repack,
                        svdq_awq_w4a16_linear, svdq_debug_group_sums,
                        svdq_debug_set_tile_policy,
@@ -38,11 +38,12 @@ from ._attention import (EXPORTS_ATTENTION, AttentionShape, KEY_BLOCK, QUERY_BLO
                          svdq_rope_tables, svdq_select_blocks, svdq_select_blocks_workspace_bytes,
                          svdq_sparse_attention, svdq_sparse_attention_workspace_bytes)
 from ._paged import (CacheEpilogue, EXPORTS_PAGED, PackedShape, PagedShape, TableShape,  # noqa: F401
-                     packed_attention, page_tables, paged_attention, qkv_norm_rope_cache,
+                     CacheStep as _CacheStep, packed_attention, page_tables, paged_attention,
+                     qkv_norm_rope_cache,
                      svdq_packed_attention, svdq_packed_attention_workspace_bytes,
                      svdq_page_tables, svdq_paged_attention,
                      svdq_paged_attention_workspace_bytes, svdq_qkv_norm_rope_cache)
-from ._tensors import BF16, F32, I32, U8, expect, on, one_device
+from ._tensors import BF16, F32, I32, U8, at, expect, on, one_device
 from ._int8 import (EXPORTS_I8, I8Linear, i8_gemm, i8_linear, i8_pack_weights,  # noqa: F401
                     i8_quantize_act, svdq_i8_gemm, svdq_i8_gemm_workspace_bytes, svdq_i8_linear,
                     svdq_i8_linear_workspace_bytes, svdq_i8_pack_weights, svdq_i8_quantize_act)
@@ -281,6 +282,19 @@ def _expect_layer(layer: dict, what: str, K: int, N: Optional[int]) -> dict:
     return tensors
 
 
+def _check_layer(layer: dict, M: int) -> None:
+    """What svdq_linear would refuse of M rows on a layer that _expect_layer has seen, refused
+    without a launch."""
+    lam, L1, L2 = layer["lam"], layer["L1"], layer["L2"]
+    r = _rank(L1, 1)
+    if r == 0:
+        L1 = L2 = None
+    row = 16                                       # stands for X and Y: looked at, never followed
+    _check_without_workspace(load_library().svdq_linear(
+        row, at(lam), at(L1), at(layer["qw"]), at(layer["sw"]), at(L2), at(layer.get("bias")), ACT_NONE, M,
+        scale_rows(layer["sw"]), lam.shape[0], r, row, None, 0, None), "svdq_linear")
+
+
 def attention(X, qkv: dict, out: dict, heads: int, head_dim: int, seq: int, gamma_q, gamma_k,
               eps: float, cos_t, sin_t, keep: int, first: int = 0,
               kv_len: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -322,8 +336,8 @@ def cached_attention(X, qkv: dict, out: dict, heads: int, kv_heads: int, head_di
     svdq_paged_attention and svdq_linear.  X bf16 [T, K]: the new tokens of all requests; the qkv
     layer has (heads + 2 kv_heads) head_dim channels; the caches get the new keys and values.
     q_starts, kv_len, slots and positions from page_tables; the other arguments as for
-    qkv_norm_rope_cache and paged_attention.  Rows of no request are unspecified.  Every tensor and
-    max_new are checked first."""
+    qkv_norm_rope_cache and paged_attention.  Rows of no request are unspecified.  Every argument is
+    checked first: a call that is refused leaves the caches as they were."""
     T, K = expect(X, "X", BF16, (None, None))
     HD = heads * head_dim
     pages, _, page, _ = expect(k_cache, "k_cache", BF16, (None, kv_heads, None, head_dim))
@@ -344,15 +358,15 @@ def cached_attention(X, qkv: dict, out: dict, heads: int, kv_heads: int, head_di
             tensors[what] = g
     if max_new is not None and max_new < 1:
         raise ValueError("max_new: expected at least 1, got %d" % max_new)
+    # (the first step, svdq_linear of qkv, checks its own before it launches anything)
+    step = _CacheStep(T, heads, kv_heads, head_dim, gamma_q, gamma_k, eps, cos_t, sin_t, positions, slots, k_cache,
+                      v_cache, tables, q_starts, kv_len, max_new, causal, half)
+    _check_layer(out, T)
     one = len({t.get_device() for t in tensors.values()}) == 1
     dev = one_device(X=X) if one else one_device(**tensors)     # the latter raises
     with on(dev):
         P = linear(X, qkv["lam"], qkv["L1"], qkv["qw"], qkv["sw"], qkv["L2"], qkv.get("bias"))
-        Q = qkv_norm_rope_cache(P, heads, kv_heads, gamma_q, gamma_k, eps, cos_t, sin_t, positions,
-                                slots, k_cache, v_cache, half=half)
-        A = paged_attention(Q, k_cache, v_cache, tables, q_starts, kv_len, max_new=max_new,
-                            causal=causal)
-        return linear(A.view(T, HD), out["lam"], out["L1"], out["qw"], out["sw"], out["L2"],
+        return linear(step.run(P).view(T, HD), out["lam"], out["L1"], out["qw"], out["sw"], out["L2"],
                       out.get("bias"))
 
 

@@ -21,6 +21,7 @@ STATUS = {
     3: "SVDQ_ERR_MISALIGNED", 4: "SVDQ_ERR_WORKSPACE_TOO_SMALL",
     5: "SVDQ_ERR_UNSUPPORTED_DEVICE", 6: "SVDQ_ERR_HIP",
 }
+WORKSPACE_TOO_SMALL = 4
 ACT_NONE, ACT_GELU = 0, 1
 GROUP = 64
 
@@ -143,6 +144,14 @@ def _check(status: int, fn: str):
     if status != 0:
         detail = load_library().svdq_last_error().decode(errors="replace")
         raise SVDQError(status, detail, fn)
+
+
+def _check_without_workspace(status: int, fn: str):
+    """The refusals of a call that was made with no workspace: one that is too small is refused
+    after all other arguments were checked and before a device is touched, so such a call
+    checks them and does nothing else."""
+    if status != WORKSPACE_TOO_SMALL:
+        _check(status, fn)
 
 
 # ------------------------------------------------------------- raw C-ABI calls

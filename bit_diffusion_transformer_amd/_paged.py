@@ -234,3 +234,43 @@ def qkv_norm_rope_cache(qkv, heads: int, kv_heads: int, gamma_q, gamma_k, eps: f
     with on(dev):
         _entries.call("svdq_qkv_norm_rope_cache", at(qkv), ctypes.byref(epi), stream_of(dev))
     return out
+
+
+class CacheStep:
+    """qkv_norm_rope_cache and paged_attention of one layer's T rows, on tensors whose types, shapes
+    and device fit together: what either would refuse is refused here, without a launch."""
+
+    def __init__(self, T: int, heads: int, kv_heads: int, head_dim: int, gamma_q, gamma_k, eps: float, cos_t,
+                 sin_t, positions, slots, k_cache, v_cache, tables, q_starts, kv_len, max_new, causal: bool,
+                 half: bool):
+        rows, pairs = cos_t.shape
+        B, width = tables.shape
+        pages, _, page, _ = k_cache.shape
+        tabs = [at(cos_t), at(sin_t), at(positions), at(slots)]
+        caches, lists = [at(k_cache), at(v_cache)], [at(tables), at(q_starts), at(kv_len)]
+        gammas = [at(gamma_q), at(gamma_k)]
+        self._q = (T, heads, head_dim)
+        # (no tokens yet: the sizes are checked, the addresses are not)
+        self._epi = CacheEpilogue(0, rows, pages, heads, kv_heads, head_dim, 2 * pairs, bool(half), page, *gammas,
+                                  eps, *tabs, None, *caches)
+        _entries.call("svdq_qkv_norm_rope_cache", None, ctypes.byref(self._epi), None)
+        if (tabs[0] | tabs[1] | caches[0] | caches[1] | (gammas[0] or 0) | (gammas[1] or 0)) & 15 or (
+                tabs[2] | tabs[3] | lists[0] | lists[1] | lists[2]) & 3:
+            raise ValueError("the caches, the rotary tables and gamma must be 16-byte aligned, lengths and tables 4-byte")
+        self._shape = PagedShape(T, pages, heads * head_dim, B, heads, kv_heads, head_dim, page, width,
+                                 _max_new(max_new, T), bool(causal))
+        self._need = svdq_paged_attention_workspace_bytes(self._shape)
+        self._rest = [*caches, *lists, ctypes.byref(self._shape), _scale(None, head_dim)]
+        if self._need == 0 and T and B:            # refused for its sizes, whatever the tensors
+            _entries.call("svdq_paged_attention", None, *self._rest, None, None, 0, None)
+
+    def run(self, qkv: torch.Tensor) -> torch.Tensor:
+        """A projection bf16 [T, (heads + 2 kv_heads) head_dim] on the current device -> the
+        attention's rows bf16 [T, heads, head_dim]; its keys and values are in the caches then."""
+        q, out = torch.empty((2,) + self._q, dtype=torch.bfloat16, device=qkv.device)
+        ws = scratch(None, self._need, qkv.device)
+        stream = stream_of(qkv.device)
+        self._epi.tokens, self._epi.q = self._q[0], at(q)
+        _entries.call("svdq_qkv_norm_rope_cache", at(qkv), ctypes.byref(self._epi), stream)
+        _entries.call("svdq_paged_attention", at(q), *self._rest, at(out), at(ws), self._need, stream)
+        return out
