@@ -59,11 +59,14 @@ int32_t read_pages(int32_t page, int64_t pages, int64_t width, int &shift) {
     return SVDQ_OK;
 }
 
-// The line of all tiles has to fit 52 bits (span_plan.h).
-int32_t check_line(const SpanArgs &a) {
+// The line of all tiles (span_plan.h) is exact in 64-bit floating point: whole numbers, over a
+// cache quarters.  At most T group / R + B tiles of a key head, R >= 16 rows; a tile's
+// length is at most (Tk + T + 512) group + 256.
+int32_t check_line(SpanArgs &a) {
     const double tiles = (double)a.T * a.group / 16 + a.B;
-    const double each = a.group * ((double)a.Tk + 256) + (double)a.T * a.group + 256;
-    if (tiles * each * a.G > 0x1p52)
+    const double each = a.group * ((double)a.Tk + (double)a.T + 512) + 256;
+    a.line = tiles * each * a.G;
+    if (a.line > (a.max_new > 0 ? 0x1p51 : 0x1p52))
         return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "%lld rows of %d sequences over %lld keys are too many",
                     (long long)a.T, a.B, (long long)a.Tk);
     return SVDQ_OK;

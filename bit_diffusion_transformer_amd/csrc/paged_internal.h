@@ -25,6 +25,7 @@ struct SpanArgs {
     float scale_log2;                    // scale log2(e)
     float inv_group_f;                   // 1 / group
     double inv_group;
+    double line;                         // the most that ascending starts can make of it (span_plan.h)
 };
 
 // Tiles of 128 or 256 rows; paged with at most 32 rows of a request and key head: a wave each.

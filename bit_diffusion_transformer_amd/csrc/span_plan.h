@@ -11,13 +11,15 @@
 // tiles see all keys give every worker the same time, without the host knowing
 // a length.
 //
-// Positions are in keys times group, whole numbers below 2^52 in 64-bit floating
-// point (exact; a 64-bit integer product or quotient takes many times as long, and
-// a short call is mostly this): tile t of a sequence is c0 + S t long (S = R with
-// `causal`: R rows are R / group tokens, so many more keys; S = 0 without).  Cuts
-// are anywhere, but every worker computes them in the same way.  More than 64 sequences
-// are measured in 64 ranges, a lane each, and searched in two levels: 2048 requests over 100
-// keys, 8 heads on 2 of 128, 47 us (59 in chunks of 64), 8192 213 (286).
+// Positions are in keys times group, whole numbers up to 2^52 or (with narrow tiles) quarters up
+// to 2^51, in 64-bit floating point (exact; a 64-bit integer product or quotient takes many times
+// as long, and a short call is mostly this).  A shape that could make the line longer is
+// refused, and a line longer than any ascending starts make it is not worked on, so every
+// worker finds the same tiles.  Tile t of a sequence is c0 + S t long (S = R with `causal`: R
+// rows are R / group tokens, so many more keys; S = 0 without).  Cuts are anywhere, but every
+// worker computes them in the same way.  More than 64 sequences are measured in 64 ranges, a
+// lane each, and searched in two levels: 2048 requests over 100 keys, 8 heads on 2 of 128, 47 us
+// (59 in chunks of 64), 8192 213 (286).
 #pragma once
 
 #include "paged_internal.h"
@@ -267,7 +269,7 @@ struct Piece {
         at.seqs = lds;
         const double sum = at.measure(a);
         total = uniform(at.head * a.G);
-        if (!(total > 0.0)) return false;
+        if (!(total > 0.0 && total <= a.line)) return false;
         const double n = total * a.inv_group * (1.0 / (kLeast<R> * kKeys));
         workers = uniform(n < 1.0 ? 1 : n < (double)most ? (int)n : most);
         if (w >= workers) return false;

@@ -73,7 +73,8 @@ size_t svdq_packed_attention_workspace_bytes(const svdq_packed_shape *shape);
  *             left as they were
  * Starts are clamped to 0 .. T (tokens_k); a sequence that ends before it starts
  * has no rows.  Where starts descend, rows of several sequences hold the result
- * of one of them, or of a mixture.
+ * of one of them, or of a mixture; no row is written where that is more work
+ * than ascending starts can name.
  * Products in bf16 with fp32 sums; the softmax in fp32 with the running maximum
  * and sum; its weights are rounded once to bf16 for the product with v; one
  * rounding of the result to bf16.  A key that a row does not see takes no part
