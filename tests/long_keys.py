@@ -9,6 +9,7 @@ import torch
 
 BF = torch.bfloat16
 LN2 = float(torch.tensor(math.log(2.0), dtype=torch.float32))
+THIRD = float(torch.tensor(math.log(2.0) / 3, dtype=torch.float32))
 
 
 def visible(n, m, causal, dead=None, device="cpu"):
@@ -106,6 +107,32 @@ def peaked(n, m, H, G, D, peaks, device="cpu"):
         away = (at - peaks[g]).abs()
         k[:, g, 0], k[:, g, 1] = (away // 256).to(BF), (away % 256).to(BF)
     return q, k, positive(5, m, G, D, device=device)
+
+
+def far(n, m, H, G, D, seed, device="cpu"):
+    """Scores of 3 a 2^22 + j, a = 1, -1 or 0 from row to row and j = 0 .. -120 from key to key, exact in
+    fp32, scale log 2 / 3 (THIRD): exponents in the millions in steps of a third.  In each block of
+    64 keys the largest j is another one (0 .. -4), so that partial results have other maxima, and v
+    is 1 or 2 for a whole block and column, so that a wrong weight of a part shows."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.zeros(n, H, D, dtype=BF, device=device)
+    a = torch.tensor([1.0, -1.0, 0.0])[torch.randint(0, 3, (n, H), generator=g)]
+    q[..., 0], q[..., 1] = (192 * a).to(device).to(BF), 1.0
+    k = torch.zeros(m, G, D, dtype=BF, device=device)
+    blocks = -(-m // 64)
+    j = torch.randint(-120, 1, (m, G), generator=g)
+    least = torch.randint(0, 5, (blocks, G), generator=g).repeat_interleave(64, 0)[:m]
+    k[..., 0], k[..., 1] = 65536.0, (j - least).clamp(min=-120).to(device).to(BF)
+    v = torch.randint(1, 3, (blocks, G, D), generator=g).repeat_interleave(64, 0)[:m].to(device).to(BF)
+    return q, k, v
+
+
+def check_thirds(out, ref, size, what=""):
+    """Weights of 2^(i / 3): each rounded to bf16 (2^-8 of sum p |v|), otherwise as check_powers.  An
+    offset of 2^22 rounded to fp32 is off by up to a quarter: by 19 % of a part."""
+    err = (out.double() - ref).abs()
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -13) * size
+    assert bool((err <= tol).all()), "%s: worst %.3g of the bound" % (what, float((err / (tol + 1e-30)).max()))
 
 
 # ------------------------------------------------------------------ pages

@@ -93,6 +93,16 @@ def test_peaks(H, G, D, page, new, lens, causal):
             lk.check_powers(out[b], ref, size, "sequence %d" % b)
 
 
+@cases
+def test_far_scores(H, G, D, page, new, lens):
+    made = [lk.far(n, m, H, G, D, 30 + b, device=DEV) for b, (n, m) in enumerate(zip(new, lens))]
+    outs = outputs(*zip(*made), page, new, lens, True, lk.THIRD)
+    for b, (n, m) in enumerate(zip(new, lens)):
+        ref, size = lk.exact(*made[b], lk.THIRD, lk.visible(n, m, True, device=DEV))
+        for out in outs:
+            lk.check_thirds(out[b], ref, size, "sequence %d" % b)
+
+
 @pytest.mark.parametrize("H,G,D,page,new,lens", [c for c in CASES if c[3]], ids=[i for c, i in zip(CASES, CASES_IDS) if c[3]])
 def test_pages_that_are_missing(H, G, D, page, new, lens):
     """Their keys would outscore all others, with values of a hundred."""

@@ -101,6 +101,19 @@ def test_peaks(m):
         lk.check_powers(model(q, k, v, lk.LN2, later), ref, size)
 
 
+@pytest.mark.parametrize("m", [150, 3000])
+def test_far_scores(m):
+    q, k, v = lk.far(7, m, 4, 2, 128, 3)
+    sees = lk.visible(7, m, False)
+    ref, size = lk.exact(q, k, v, lk.THIRD, sees)
+    lk.check_thirds(model(q, k, v, lk.THIRD, sees), ref, size)
+    for out in (model(q, k, v, lk.THIRD, sees, near_only=True), model(q, k, v, lk.THIRD, sees, blind_join=True),
+                model(q, k, v, lk.THIRD, sees, taken(m, slice(0, 64), 0)),
+                model(q, k, v, lk.THIRD, sees, taken(m, slice(64, 128), 2)), torch.zeros_like(q)):
+        with pytest.raises(AssertionError):
+            lk.check_thirds(out, ref, size)
+
+
 def test_a_page_that_is_missing():
     """Its keys outscore all others and have large values: any weight on them shows."""
     m, H, D = 9000, 4, 64
