@@ -110,6 +110,11 @@ def _out(out: Optional[torch.Tensor], q: torch.Tensor, what: str = "out") -> tor
     return out
 
 
+def _range(sizes: dict) -> None:
+    """The error of sizes of which one is no C int32 (ctypes would drop its higher bits)."""
+    raise ValueError("out of range: %s" % ", ".join("%s = %d" % x for x in sizes.items()))
+
+
 def _scale(scale: Optional[float], D: int) -> float:
     return max(D, 1) ** -0.5 if scale is None else scale
 
@@ -136,6 +141,8 @@ def packed_attention(q, k, v, q_starts, k_starts: Optional[torch.Tensor] = None,
     B = expect(q_starts, "q_starts", I32, (None,))[0] - 1
     if B < 0:
         raise ValueError("q_starts: expected at least one entry")
+    if (B | H | G | D) >> 31:
+        _range(dict(sequences=B, heads=H, kv_heads=G, head_dim=D))
     if k_starts is not None:
         expect(k_starts, "k_starts", I32, (B + 1,))
     elif Tk != T:
@@ -166,6 +173,8 @@ def paged_attention(q, k_cache, v_cache, tables, q_starts, kv_len, max_new: Opti
     B, width = expect(tables, "tables", I32, (None, None))
     expect(q_starts, "q_starts", I32, (B + 1,))
     expect(kv_len, "kv_len", I32, (B,))
+    if (B | H | G | D | page | width) >> 31:
+        _range(dict(requests=B, heads=H, kv_heads=G, head_dim=D, page=page, width=width))
     out = _out(out, q)
     dev = one_device(q=q, k_cache=k_cache, v_cache=v_cache, tables=tables, q_starts=q_starts,
                      kv_len=kv_len, out=out)
@@ -192,6 +201,8 @@ def page_tables(cached, added, free_pages, tables, page: int, pages: int, tokens
     width = expect(tables, "tables", I32, (B, None))[1]
     if not 0 <= tokens < 1 << 31 or not 0 <= pages < 1 << 31 or not 0 < page <= MAX_PAGE:
         raise ValueError("page = %d, pages = %d, tokens = %d" % (page, pages, tokens))
+    if (B | width) >> 31:
+        _range(dict(requests=B, width=width))
     dev = one_device(cached=cached, added=added, free_pages=free_pages, tables=tables)
     q_starts, kv_len, slots, positions, counts = torch.split_with_sizes(
         cached.new_empty(2 * (B + tokens) + 3), (B + 1, B, tokens, tokens, 2))
@@ -222,6 +233,8 @@ def qkv_norm_rope_cache(qkv, heads: int, kv_heads: int, gamma_q, gamma_k, eps: f
     expect(sin_t, "sin_t", F32, (rows, pairs))
     expect(positions, "positions", I32, (T,))
     expect(slots, "slots", I32, (T,))
+    if (heads | kv_heads | D | 2 * pairs | page) >> 31:
+        _range(dict(heads=heads, kv_heads=kv_heads, head_dim=D, rotary=2 * pairs, page=page))
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=qkv.device)
     else:
@@ -246,6 +259,9 @@ class CacheStep:
         rows, pairs = cos_t.shape
         B, width = tables.shape
         pages, _, page, _ = k_cache.shape
+        if (B | heads | kv_heads | head_dim | 2 * pairs | page | width) >> 31:
+            _range(dict(requests=B, heads=heads, kv_heads=kv_heads, head_dim=head_dim, rotary=2 * pairs, page=page,
+                        width=width))
         tabs = [at(cos_t), at(sin_t), at(positions), at(slots)]
         caches, lists = [at(k_cache), at(v_cache)], [at(tables), at(q_starts), at(kv_len)]
         gammas = [at(gamma_q), at(gamma_k)]
