@@ -68,7 +68,10 @@ size_t svdq_packed_attention_workspace_bytes(const svdq_packed_shape *shape);
  *             q_starts (then tokens_k == tokens_q)
  *   scale     > 0 and at most 2^127 (usually D^-1/2); the sum of |q[d] k[d]| over
  *             d, and scale times it, below 2^126 (a larger one may pass what
- *             fp32 holds and give NaN)
+ *             fp32 holds and give NaN); the sum of |v| over the keys of a row below
+ *             2^119 in each column (the sums of weights times v are divided by the
+ *             weights' at the end, and a weight is at most 2^8; a larger one may give
+ *             an infinity or NaN)
  *   out       device bf16 [T][H][D] (out), contiguous; rows of no sequence are
  *             left as they were
  * Starts are clamped to 0 .. T (tokens_k); a sequence that ends before it starts
@@ -197,7 +200,8 @@ typedef struct svdq_cache_epilogue {
 
 /*
  * qkv device bf16 [T][(H + 2 G) D], contiguous.  Norm and turn in fp32, one
- * rounding to bf16; V is copied.  A token whose slot is outside 0 .. pages *
+ * rounding to bf16 (a head whose squares add up to 2^128 or more gives zeros); V
+ * is copied.  A token whose slot is outside 0 .. pages *
  * page - 1 leaves the cache as it was; one whose position is outside the tables
  * (rows behind the last request) leaves its row of q and the cache as they were.
  * Slots of the call's tokens must be distinct (of equal ones the cache row holds
