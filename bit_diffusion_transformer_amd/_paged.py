@@ -165,7 +165,7 @@ def paged_attention(q, k_cache, v_cache, tables, q_starts, kv_len, max_new: Opti
     """Attention of new tokens over a paged cache: q bf16 [T, H, D], caches bf16 [pages, G, page, D],
     tables int32 [requests, width] of page numbers, q_starts int32 [requests + 1], kv_len int32
     [requests] (the new tokens' keys, already in the cache, included) -> bf16 [T, H, D].  max_new:
-    the most new tokens of a request, if known (1 when decoding).  causal, scale and out as for
+    the most new tokens of a request, if known (1 when decoding; without it up to a fifth slower).  causal, scale and out as for
     packed_attention."""
     (T, H, D), qs = expect_rows(q, "q", BF16, (None, None, None))
     pages, G, page, _ = expect(k_cache, "k_cache", BF16, (None, None, None, D))

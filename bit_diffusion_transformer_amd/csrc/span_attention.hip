@@ -12,13 +12,15 @@
 //
 // What bounds it.  Long sequences: power.  16384 causal tokens, 32 heads on 8 of 128, take 2.0 ms
 // (1.1 PFLOP/s, the matrix units busy 54 % of the cycles at about 1.9 GHz); with all inputs zero
-// the same cycles take 1.64 ms.  Two streams of 1560 rows over 32760 keys, 12 heads: 670 us, 0.89
-// PFLOP/s.  Short ones: a tile's start and end (the queries, the first copies, the partial
-// results; about 4 us), which other workgroups of the compute unit fill in part: twelve prompts
-// of 1 to 2000 tokens 98 us, 0.67 PFLOP/s.  Two waves a SIMD, D = 64 too: with four (and 128
-// registers) its pass spills, 1000 causal tokens of 16 heads 29.7 us against 22.2, 4000 80 against
-// 66.  Narrow: 31 decoding requests of up to 6000 keys beside 512 new tokens over 4608, 28 heads of
-// 64 on 4, in tiles of 256 rows: 48 us, 54 with wide tiles for all; the 31 alone 20 and 26.
+// the same work takes 1.54 ms.  Four images of 777 to 4096 tokens, 24 heads: 310 us, with zeros 246.
+// Two streams of 1560 rows over 32760 keys, 12 heads: 670 us, 0.89 PFLOP/s, with zeros 515.  (On the
+// slowest card seen 2.16 ms, 333 and 721 us.)  Short ones: a tile's start and end (the queries, the
+// first copies, the partial results; about 4 us), which other workgroups of the compute unit fill
+// in part: twelve prompts of 1 to 2000 tokens 100 us, 0.66 PFLOP/s (90 with zeros).  Two waves a
+// SIMD, D = 64 too: with four (and 128 registers) its pass spills, 1000 causal tokens of 16 heads
+// 29.7 us against 22.2, 4000 80 against 66.  Narrow: 31 decoding requests of up to 6000 keys beside
+// 512 new tokens over 4608, 28 heads of 64 on 4, in tiles of 256 rows: 48 us, 54 with wide tiles for
+// all; the 31 alone 20 and 26.
 #include "attention_tile.h"
 #include "span_plan.h"
 
@@ -61,7 +63,7 @@ span_attention_kernel(SpanArgs a, Shared *__restrict__ shared, float *__restrict
     if (!piece.open(a, lds.seqs[wave], w, (int)gridDim.x)) return;
     Place<kRows> &at = piece.at;
 
-    // Within the 16 rows that this wave copies of a block: bytes of a row from the first.
+    // Within the 16 or 8 rows that this wave copies of a block: bytes of a row from the first.
     const int cp_row = lane / SEGS, cp_slot = lane % SEGS;
     const int64_t k_row = PAGED ? D * 2 : a.k_stride * 2, v_row = PAGED ? D * 2 : a.v_stride * 2;
     uint32_t k_at[COPIES], v_at[COPIES];
@@ -656,8 +658,8 @@ join_tiles_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__
     }
 }
 
-// Workers: as many workgroups as the compute units hold at once, two waves to a SIMD (four
-// at D = 64), or fewer where even the most keys that the shape allows make fewer pieces.
+// Workers: as many workgroups as the compute units hold at once, two waves to a SIMD, or fewer
+// where even the most keys that the shape allows make fewer pieces.
 template <int D, int WAVES>
 int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, 2048 / WAVES); }
 
@@ -670,6 +672,10 @@ int workers(const SpanArgs &a) { return span_workers<32 * WAVES>(a, 2048 / WAVES
 // 65.9, 48 decoding requests and 1000 new 82 | 78; D = 64: 28 heads on 4, 512 over 4608 beside
 // 31 decoding requests 46 | 49, 48 decoding and 1000 new 31 | 37; 12 heads, 2 x 1560 over 32760
 // 425 | 406; 32 on 4, 2048 over 20000 406 | 373.
+// The lengths are the device's alone, so the rule for packed ones takes their mean, and a long sequence
+// among many short or empty ones gets tiles of 128: 16384 tokens beside 40 of one token 2160 | 1960,
+// 8192 beside them 566 | 522, the four images beside 28 empty ones 335 | 306 (beside 8 of 500 tokens
+// 16384 pass the rule).
 bool wide(const SpanArgs &a) {
     if (a.max_new > 0) return (double)a.T * a.H * a.D >= 0x1p21;
     const double pairs = (double)a.T * (double)a.Tk / a.B * a.H;

@@ -419,7 +419,7 @@ join_rows_kernel(SpanArgs a, const Shared *__restrict__ shared, const float *__r
 // Workers: two to a compute unit (four at D = 64), which keep enough copies in flight, or
 // twice as many where there is a tile for each.  D = 128, 512 | 1024 workers, us with the join:
 // one token over 65537 keys 58 | 63, 64 over 9 to 8192 72 | 74, 256 over 1000 197 | 192, 256 over
-// 4000 723 | 708; D = 64, 1024 | 2048: one over 65537 32 | 40.
+// 4000 723 | 708; D = 64, 1024 | 2048: one over 65537 37 | 43.
 template <int D, int NR>
 int workers(const SpanArgs &a) {
     const int64_t tiles = (a.B < a.T ? a.B : a.T) * (int64_t)a.G;

@@ -106,7 +106,9 @@ typedef struct svdq_paged_shape {
     int32_t page;        /* tokens of a page: a power of two, 16 .. 256 */
     int32_t width;       /* entries of a table row, >= 0; width * page <= SVDQ_MAX_SLOTS */
     int32_t max_new;     /* the most new tokens of a request, >= 1: chooses the kernel; a
-                            request with more is computed all the same, slower */
+                            request with more is computed all the same, slower, and
+                            so are requests with far fewer (64 with one token each
+                            over up to 8192 keys: 70 us with 1, 85 with 64) */
     int32_t causal;      /* 0 or 1 */
 } svdq_paged_shape;
 
