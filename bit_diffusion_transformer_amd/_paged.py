@@ -165,8 +165,8 @@ def paged_attention(q, k_cache, v_cache, tables, q_starts, kv_len, max_new: Opti
     """Attention of new tokens over a paged cache: q bf16 [T, H, D], caches bf16 [pages, G, page, D],
     tables int32 [requests, width] of page numbers, q_starts int32 [requests + 1], kv_len int32
     [requests] (the new tokens' keys, already in the cache, included) -> bf16 [T, H, D].  max_new:
-    the most new tokens of a request, if known (1 when decoding; without it up to a fifth slower).  causal, scale and out as for
-    packed_attention."""
+    the most new tokens of a request, if known (1 when decoding, which is up to a fifth slower
+    without it).  causal, scale and out as for packed_attention."""
     (T, H, D), qs = expect_rows(q, "q", BF16, (None, None, None))
     pages, G, page, _ = expect(k_cache, "k_cache", BF16, (None, None, None, D))
     expect(v_cache, "v_cache", BF16, (pages, G, page, D))
@@ -272,7 +272,8 @@ class CacheStep:
         _entries.call("svdq_qkv_norm_rope_cache", None, ctypes.byref(self._epi), None)
         if (tabs[0] | tabs[1] | caches[0] | caches[1] | (gammas[0] or 0) | (gammas[1] or 0)) & 15 or (
                 tabs[2] | tabs[3] | lists[0] | lists[1] | lists[2]) & 3:
-            raise ValueError("the caches, the rotary tables and gamma must be 16-byte aligned, lengths and tables 4-byte")
+            raise ValueError("the caches, the rotary tables and gamma must be 16-byte aligned, lengths "
+                             "and tables 4-byte")
         self._shape = PagedShape(T, pages, heads * head_dim, B, heads, kv_heads, head_dim, page, width,
                                  _max_new(max_new, T), bool(causal))
         self._need = svdq_paged_attention_workspace_bytes(self._shape)

@@ -17,7 +17,8 @@ constexpr int kStep = 256 * kPer;      // pieces per workgroup
 // half layout the partner of a lane's piece is the piece rotary / 16 lanes
 // further (or back), one lane exchange for each of its 8 values.  8000 tokens of 32 heads on 4 of
 // 128, a quarter turned: 39 us, 4.2 TB/s (all turned, tables of 8000 rows: 37, in halves 40); 64
-// tokens of 32 on 8 6.4 us, the launch and three dependent loads.  Four pieces a thread, all loaded first, keep enough in flight for that.
+// tokens of 32 on 8 6.4 us, the launch and three dependent loads.  Four pieces a thread, all
+// loaded first, keep enough in flight for that.
 template <int D, bool HALF>
 __global__ void __launch_bounds__(256)
 cache_rope_kernel(CacheArgs a) {

@@ -203,9 +203,9 @@ typedef struct svdq_cache_epilogue {
 /*
  * qkv device bf16 [T][(H + 2 G) D], contiguous.  Norm and turn in fp32, one
  * rounding to bf16 (a head whose squares add up to 2^128 or more gives zeros); V
- * is copied.  A token whose slot is outside 0 .. pages *
- * page - 1 leaves the cache as it was; one whose position is outside the tables
- * (rows behind the last request) leaves its row of q and the cache as they were.
+ * is copied.  A token whose slot is outside 0 .. pages * page - 1 leaves the cache
+ * as it was; one whose position is outside the tables (rows behind the last
+ * request) leaves its row of q and the cache as they were.
  * Slots of the call's tokens must be distinct (of equal ones the cache row holds
  * a mixture).
  */
