@@ -1,5 +1,6 @@
 """A v that is not finite shows in its column of every row that sees its key, also where the
 key's weight underflows to zero, wherever in a block of keys, beside a mask or not."""
+import numpy as np
 import pytest
 import torch
 
@@ -79,3 +80,34 @@ def test_paged(H, G, D, new, lens, missing, bad):
             vb[int(tables[b, (n - back) // page]), :, (n - back) % page, 3] = bad
         out = bdt.paged_attention(q, kb, vb, *args, max_new=max(new), scale=scale)
         compare(out, clean, sees)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_values_show_where_their_keys_are_seen(seed):
+    """Some values of some keys are not finite, and most weights are zero: a column of a row is finite
+    where the row sees none of them, and nowhere else."""
+    rng = np.random.default_rng(seed)
+    G = int(rng.choice([1, 2, 4]))
+    H, D, page = G * int(rng.choice([1, 2, 4, 8])), int(rng.choice([64, 128])), int(rng.choice([16, 32, 64]))
+    causal, B, most = bool(rng.integers(2)), int(rng.integers(1, 6)), int(rng.choice([1, 4, 200, 900]))
+    new = rng.integers(1, most + 1, B).tolist()
+    lens = [int(n + rng.integers(0, 1 + int(rng.choice([3, 100, 1500])))) for n in new]
+    q, kc, vc, tables, ks, vs = paged_inputs(H, G, D, page, new, lens, 50 + seed, gain=40.0)
+    odd = []
+    for b, n in enumerate(lens):
+        odd.append(torch.zeros(n, G, D, dtype=torch.bool, device=DEV))
+        for _ in range(1 + n // 200):
+            j, g, d = int(rng.integers(n)), int(rng.integers(G)), int(rng.integers(D))
+            vs[b][j, g, d] = BAD[int(rng.integers(3))]
+            vc[tables[b, j // page], g, j % page, d] = vs[b][j, g, d]
+            odd[b][j, g, d] = True
+    at, kv = starts_of(new), ints(lens)
+    outs = [bdt.paged_attention(q, kc, vc, tables, ints(at), kv, max_new=m, causal=causal) for m in (max(new), None, 1)]
+    outs.append(bdt.packed_attention(q, torch.cat(ks), torch.cat(vs), ints(at), ints(starts_of(lens)), causal=causal))
+    for b, (n, m) in enumerate(zip(new, lens)):
+        key, row = torch.arange(m, device=DEV), torch.arange(n, device=DEV)
+        sees = key[None, :] <= row[:, None] + (m - n) if causal else torch.ones(n, m, dtype=torch.bool, device=DEV)
+        want = torch.einsum("nm,mgd->ngd", sees.float(), odd[b].float()) > 0
+        want = want.repeat_interleave(H // G, 1)
+        for out in outs:
+            assert torch.equal(~torch.isfinite(out[at[b]:at[b + 1]]), want), "request %d" % b
